@@ -59,29 +59,29 @@ _GROUPED = {"scoring": "sigmoid", "groups": 8, "topk_groups": 4, "group_top": 2,
 def listed():
     return [
         # one new token of one request: latency
-        _route("route", "route, 1 token", 1, 8, 2),
+        _route("route", "route 1 token", 1, 8, 2),
         # a serving batch under a sigmoid router with a balance bias and groups, bf16 logits
-        _route("route", "route, decode batch", 250, 64, 8, dtype="bf16", **_GROUPED),
+        _route("route", "route decode batch", 250, 64, 8, dtype="bf16", **_GROUPED),
         # a long prefill (or training batch) over many experts
-        _route("route", "route, prefill", 16384, 256, 8, **_GROUPED),
+        _route("route", "route prefill", 16384, 256, 8, **_GROUPED),
         # one layer of a padded training batch at the 8-expert configuration
-        _route("losses", "losses, 8 experts", 4096, 8, 2, masked=0.15),
+        _route("losses", "losses 8 experts", 4096, 8, 2, masked=0.15),
         # the concatenated logits of several layers, many experts
-        _route("losses", "losses, 64 experts", 65521, 64, 6, masked=0.05),
+        _route("losses", "losses 64 experts", 65521, 64, 6, masked=0.05),
         # the gradient that goes with the first of these: weights, balance and z terms
-        _route("route_backward", "route backward, 8 experts", 4096, 8, 2, masked=0.15),
+        _route("route_backward", "route backward 8 experts", 4096, 8, 2, masked=0.15),
         # and of the grouped sigmoid router
-        _route("route_backward", "route backward, 256 experts", 16384, 256, 8, **_GROUPED),
+        _route("route_backward", "route backward 256 experts", 16384, 256, 8, **_GROUPED),
         # gradient of the combine for a small batch of a router that is being tuned
-        _combine("combine backward, 16 tokens", 16, 4096, 2, 8),
+        _combine("combine backward 16 tokens", 16, 4096, 2, 8),
         # and for a training sequence
-        _combine("combine backward, 4096 tokens", 4096, 4096, 2, 8),
+        _combine("combine backward 4096 tokens", 4096, 4096, 2, 8),
         # one token's two routed rows beside the down projection of the experts
-        _lora("lora, 2 rows", 2, 14336, 4096, 16, 64, "fp32", "mixed"),
+        _lora("lora 2 rows", 2, 14336, 4096, 16, 64, "fp32", "mixed"),
         # a decode batch, a request per row, beside a bf16 projection
-        _lora("lora, 61 rows", 61, 4096, 14336, 16, 128, "bf16", "mixed"),
+        _lora("lora 61 rows", 61, 4096, 14336, 16, 128, "bf16", "mixed"),
         # prefill of a few long requests beside the gate (or up) projection, fp32 sums
-        _lora("lora, 4096 rows", 4096, 4096, 14336, 64, 16, "fp32", "runs"),
+        _lora("lora 4096 rows", 4096, 4096, 14336, 64, 16, "fp32", "runs"),
     ]
 
 
