@@ -439,6 +439,87 @@ moe_status_t moe_combine_peer(const float* const* y_bases, int world, int64_t y_
                               int64_t num_tokens, int k, int hidden, int32_t* bad_slots,
                               moe_stream_t stream);
 
+/* ---- General routing, router losses and their gradients ----
+ * Mixtral's router is one rule (float32 softmax, top-k on the logits, renormalised). These
+ * entry points take the router's logits and cover the rules other sparse layers use, and
+ * what tuning a router beside frozen experts needs: the two router losses (Hugging Face
+ * "Mixtral", MixtralConfig: router_aux_loss_coef) and the gradient in the logits.
+ *
+ * For a token with logits l[0..E):
+ *   s       = softmax(l) over all E, or sigmoid(l) elementwise  (scoring)
+ *   c       = s + select_bias                                   (selection only)
+ *   groups: experts are cut into num_groups runs of E / num_groups; a group's value is the
+ *           sum of its group_top largest c; the topk_groups groups of largest value stay
+ *   idx     = the k largest c of the groups that stay, slot 0 the largest
+ *   w[j]    = weight_scale * s[idx[j]]  (divided by sum_j s[idx[j]] when renormalize)
+ * Every comparison is decided as if s, c and the group values were computed without
+ * rounding error (values within double precision of each other count as equal); equal
+ * values go to the lower index. With no select_bias, experts are compared by
+ * their logits.
+ * A NaN logit counts as -infinity, and a logit of +infinity as the largest float. An
+ * expert of logit -infinity has score 0; a NaN select_bias makes its expert's c
+ * -infinity. Experts whose c is -infinity come last, lower index first. Slots whose
+ * scores sum to 0 have weight 0 where renormalised. */
+#define MOE_SCORING_SOFTMAX 0
+#define MOE_SCORING_SIGMOID 1
+
+/* Sizes: num_tokens >= 0 (0: nothing is launched), 1 <= num_experts <= 512,
+ * 1 <= num_experts_per_tok <= min(32, topk_groups * E / num_groups), num_groups <= 32
+ * divides num_experts, 1 <= topk_groups <= num_groups, 1 <= group_top <= E / num_groups
+ * (one group: topk_groups = group_top = 1). logits_bf16: 0 logits are fp32, 1 bf16.
+ * logits_stride: elements from one token's logits to the next's, >= num_experts.
+ * (moe_permute takes up to 64 experts and 8 slots.) */
+typedef struct {
+  int64_t num_tokens;
+  int64_t logits_stride;
+  int32_t num_experts;
+  int32_t num_experts_per_tok;
+  int32_t scoring;
+  int32_t num_groups;
+  int32_t topk_groups;
+  int32_t group_top;
+  int32_t renormalize;
+  int32_t logits_bf16;
+  float weight_scale;
+} moe_routing_t;
+
+/* The routing above. logits [T, E] fp32 or bf16 (row stride logits_stride; aligned to its
+ * element); select_bias [E] fp32, nullable; topk_idx [T, k] int32 out; topk_w [T, k] fp32
+ * out. */
+moe_status_t moe_route(const moe_routing_t* routing, const void* logits, const float* select_bias,
+                       int32_t* topk_idx, float* topk_w, moe_stream_t stream);
+
+/* Router losses over the N tokens whose token_mask is non-zero:
+ *   p = softmax(l), or s / sum(s) with sigmoid scores;   P_e = sum_t p_te / N
+ *   f_e = counts_e / N, counts_e the slots of those tokens that name expert e
+ *   losses[0] = E * sum_e f_e * P_e             (load balancing; k for uniform routing)
+ *   losses[1] = sum_t logsumexp(l_t)^2 / N      (z-loss)
+ * Both are 0 when N = 0. Per-token terms are fp32; the sums over tokens are carried in
+ * double across blocks, in an order that the shape alone fixes.
+ *   logits as for moe_route; topk_idx [T, k] int32, distinct within a token (a value
+ *   outside [0, E) names no expert); token_mask [T] uint8, nullable (all tokens count);
+ *   losses [2] fp32 out; counts [E + 1] int32 out, counts[E] = N; prob_mean [E] fp32 out
+ *   (P); ws a device workspace of moe_router_losses_workspace() bytes (256-byte aligned;
+ *   its content does not matter). Uses only num_experts, num_experts_per_tok, scoring,
+ *   num_tokens and the logits fields of `routing`. */
+size_t moe_router_losses_workspace(const moe_routing_t* routing);
+moe_status_t moe_router_losses(const moe_routing_t* routing, const void* logits,
+                               const int32_t* topk_idx, const uint8_t* token_mask, float* losses,
+                               int32_t* counts, float* prob_mean, void* ws, size_t ws_bytes,
+                               moe_stream_t stream);
+
+/* Gradient in the logits of  sum(d_topk_w * topk_w) + d_losses . losses, the selection and
+ * the counts taken as constants:
+ *   topk_idx [T, k] int32 as moe_route chose it (a value outside [0, E) is no slot);
+ *   d_topk_w [T, k] fp32, nullable (no weight term);
+ *   counts [E + 1] int32 from moe_router_losses and d_losses [2] fp32 (device), both or
+ *     neither NULL (no loss terms); token_mask [T] uint8, nullable: the losses' mask;
+ *   d_logits [T, E] out, contiguous, of the logits' type: fp32 arithmetic, one rounding. */
+moe_status_t moe_route_backward(const moe_routing_t* routing, const void* logits,
+                                const int32_t* topk_idx, const float* d_topk_w,
+                                const int32_t* counts, const float* d_losses,
+                                const uint8_t* token_mask, void* d_logits, moe_stream_t stream);
+
 /* Waits for `stream`, then reads and clears the device status word in `ws`:
  * MOE_OK, or MOE_ERR_TIMEOUT if a kernel gave up a bounded wait since the last
  * call. */

@@ -174,12 +174,44 @@ cudaError_t launch_combine_peer(const float* const* y_bases, int world, int64_t 
                                 const float* topk_w, const uint16_t* residual, uint16_t* out,
                                 int64_t T, int H, int k, int32_t* bad, cudaStream_t st);
 
+// ---- general routing, router losses and their gradients (route.cu) ----
+
+struct Routing {
+  int64_t T, stride;     // tokens; elements from one token's logits to the next's
+  int E, k;
+  int sigmoid;           // scores: softmax over E (0) or sigmoid (1)
+  int groups, topk_groups, group_top;
+  int renorm;
+  int bf16;              // logits (and their gradient) are bf16
+  float scale;
+};
+
+cudaError_t launch_route(const Routing& r, const void* logits, const float* bias, int32_t* idx,
+                         float* w, cudaStream_t st);
+
+// Blocks of the losses' first pass: each leaves E + 1 partial sums and E + 1 counts.
+int router_loss_blocks(const Routing& r);
+cudaError_t launch_router_losses(const Routing& r, const void* logits, const int32_t* idx,
+                                 const uint8_t* mask, float* losses, int32_t* counts,
+                                 float* prob_mean, double* part_sum, int32_t* part_count,
+                                 cudaStream_t st);
+
+cudaError_t launch_route_backward(const Routing& r, const void* logits, const int32_t* idx,
+                                  const float* d_w, const int32_t* counts, const float* d_losses,
+                                  const uint8_t* mask, void* d_logits, cudaStream_t st);
+
 int num_sms();
 
 // Host helpers of the C ABI (moe_api.cu): shape validation returning a moe_status_t
 // (message in moe_last_error), and setting the thread's moe_last_error message.
 int validate_shape(const moe_shape_t* shape, Shape* out);
 void set_error_message(const char* msg);
+
+// Checks shared by the entry points outside moe_api.cu (route_api.cu): a status with its
+// message, a launch's result, and a pointer's presence and alignment.
+moe_status_t fail_with(moe_status_t code, const char* fmt, ...);
+moe_status_t launched(cudaError_t e, const char* where);
+moe_status_t check_aligned(const void* p, const char* name, size_t align, bool nullable);
 
 // ---- programmatic dependent launch ----
 // Every kernel of the layer is launched with programmatic stream serialization: it

@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -30,7 +30,8 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_size_host", "moe_max_padded_rows
            "moe_quantize_int8", "moe_grouped_swiglu_w8", "moe_forward_w8", "moe_gather_rows",
            "moe_forward_host_async", "moe_quantize_int4", "moe_grouped_swiglu_w4", "moe_forward_w4",
            "moe_ipc_alloc", "moe_ipc_open", "moe_ipc_close", "moe_ipc_free",
-           "moe_scatter_rows_peer", "moe_combine_peer")
+           "moe_scatter_rows_peer", "moe_combine_peer", "moe_route", "moe_router_losses",
+           "moe_router_losses_workspace", "moe_route_backward")
 
 
 @dataclass
@@ -85,6 +86,15 @@ class Shape(ctypes.Structure):
                 ("intermediate_size", ctypes.c_int32), ("num_experts", ctypes.c_int32),
                 ("num_experts_per_tok", ctypes.c_int32), ("weight_layout", ctypes.c_int32),
                 ("router_bf16_logits", ctypes.c_int32)]
+
+
+class _RoutingArgs(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("logits_stride", ctypes.c_int64),
+                ("num_experts", ctypes.c_int32), ("num_experts_per_tok", ctypes.c_int32),
+                ("scoring", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renormalize", ctypes.c_int32), ("logits_bf16", ctypes.c_int32),
+                ("weight_scale", ctypes.c_float)]
 
 
 _lib = None
@@ -165,6 +175,15 @@ def lib() -> ctypes.CDLL:
         L.moe_combine_peer.argtypes = [_P, ctypes.c_int, ctypes.c_int64, _P, _P, _P, _P, _P,
                                        ctypes.c_int64, ctypes.c_int, ctypes.c_int, _P, _P]
         L.moe_combine_peer.restype = st
+        rp = ctypes.POINTER(_RoutingArgs)
+        L.moe_route.argtypes = [rp, _P, _P, _P, _P, _P]
+        L.moe_route.restype = st
+        L.moe_router_losses_workspace.argtypes = [rp]
+        L.moe_router_losses_workspace.restype = _SZ
+        L.moe_router_losses.argtypes = [rp, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]
+        L.moe_router_losses.restype = st
+        L.moe_route_backward.argtypes = [rp, _P, _P, _P, _P, _P, _P, _P, _P]
+        L.moe_route_backward.restype = st
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -712,3 +731,149 @@ def combine_peer(y_bases, y_rows: int, slot_rank, slot_row, topk_w, hidden: int,
         _dev(out, "out"), t, k, hidden, _dev(bad, "bad", torch.int32, True), _stream(stream)))
     return out
 
+
+# ---- general routing, router losses and their gradients ----
+
+_SCORING = {"softmax": 0, "sigmoid": 1}
+
+
+@dataclass(frozen=True)
+class Routing:
+    """A routing rule (include/moe.h): k experts per token by softmax or sigmoid scores;
+    with num_groups > 1 only the topk_groups groups whose group_top best experts sum
+    highest are open; the weights are renormalised to sum to 1 (or not), times scale."""
+    k: int
+    scoring: str = "softmax"
+    num_groups: int = 1
+    topk_groups: int = 1
+    group_top: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
+
+
+class RouterLosses(NamedTuple):
+    """losses [2] fp32 (load balancing, z-loss); counts [E + 1] int32 (slots per expert,
+    then the tokens that count); prob_mean [E] fp32 (mean probability per expert)."""
+    losses: torch.Tensor
+    counts: torch.Tensor
+    prob_mean: torch.Tensor
+
+
+class _On:
+    """The device and stream of a call, current for its length, so that outputs and scratch
+    belong to the stream the kernels run on. device: the call's first tensor's."""
+
+    def __init__(self, device: torch.device, stream):
+        self.device, self.stream = device, stream
+        self.inside = None
+
+    def __enter__(self):
+        if self.stream is not None:
+            if self.stream.device != self.device:
+                raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
+            self.inside = torch.cuda.stream(self.stream)
+        elif self.device.index != torch.cuda.current_device():
+            self.inside = torch.cuda.device(self.device)
+        if self.inside is not None:
+            self.inside.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.inside is not None:
+            self.inside.__exit__(*exc)
+
+
+def _arg(t, name: str, dtypes, shape, device=None) -> Optional[int]:
+    """The address of a contiguous CUDA tensor of one of `dtypes` and of exactly `shape`."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+_F32, _I32, _LOGITS = (torch.float32,), (torch.int32,), (torch.float32, torch.bfloat16)
+
+
+def _routing_args(logits, routing: Routing) -> _RoutingArgs:
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [tokens, experts], got {tuple(logits.shape)}")
+    t, e = logits.shape
+    if logits.dtype not in _LOGITS:
+        raise ValueError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
+    if routing.scoring not in _SCORING:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {routing.scoring!r}")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if e > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must be contiguous along the experts")
+    stride = logits.stride(0) if t > 1 else e
+    return _RoutingArgs(t, stride, e, routing.k, _SCORING[routing.scoring], routing.num_groups,
+                        routing.topk_groups, routing.group_top, int(routing.renormalize),
+                        int(logits.dtype == torch.bfloat16), routing.scale)
+
+
+def route(logits, routing: Routing, bias=None, stream=None):
+    """(topk_idx [T, k] int32, topk_w [T, k] fp32) of router logits [T, E] (fp32 or bf16,
+    rows may be strided) under `routing`; bias [E] fp32 is added to the scores for the
+    selection only (see moe_route)."""
+    args = _routing_args(logits, routing)
+    t, e = logits.shape
+    dev = logits.device
+    b = None if bias is None else _arg(bias, "bias", _F32, (e,), dev)
+    with _On(dev, stream) as st:
+        idx = torch.empty((t, routing.k), dtype=torch.int32, device=dev)
+        w = torch.empty((t, routing.k), dtype=torch.float32, device=dev)
+        _check(lib().moe_route(args, logits.data_ptr(), b, idx.data_ptr(), w.data_ptr(), st))
+    return idx, w
+
+
+def _token_mask(mask, t: int, dev) -> Optional[int]:
+    return None if mask is None else _arg(mask, "token_mask", (torch.bool, torch.uint8), (t,), dev)
+
+
+def router_losses(logits, topk_idx, routing: Routing, token_mask=None, stream=None) -> RouterLosses:
+    """Load-balancing loss and z-loss over the tokens whose token_mask (bool or uint8 [T];
+    None: all) is true (see moe_router_losses). topk_idx [T, k] int32 as routed. A tuple
+    (losses [2], counts [E + 1], prob_mean [E])."""
+    args = _routing_args(logits, routing)
+    t, e = logits.shape
+    dev = logits.device
+    idx = _arg(topk_idx, "topk_idx", _I32, (t, routing.k), dev)
+    mask = _token_mask(token_mask, t, dev)
+    with _On(dev, stream) as st:
+        n = lib().moe_router_losses_workspace(args)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        losses = torch.empty(2, dtype=torch.float32, device=dev)
+        counts = torch.empty(e + 1, dtype=torch.int32, device=dev)
+        prob = torch.empty(e, dtype=torch.float32, device=dev)
+        _check(lib().moe_router_losses(args, logits.data_ptr(), idx, mask, losses.data_ptr(),
+                                       counts.data_ptr(), prob.data_ptr(), ws.data_ptr(), n, st))
+    return RouterLosses(losses, counts, prob)
+
+
+def route_backward(logits, topk_idx, routing: Routing, d_topk_w=None, counts=None, d_losses=None,
+                   token_mask=None, stream=None):
+    """Gradient in the logits [T, E] (their type) of sum(d_topk_w * topk_w) plus
+    sum(d_losses * losses), the selection held fixed: d_topk_w [T, k] fp32 or None; counts
+    as router_losses returned them, with d_losses [2] fp32, or both None (see
+    moe_route_backward)."""
+    args = _routing_args(logits, routing)
+    t, e = logits.shape
+    dev = logits.device
+    idx = _arg(topk_idx, "topk_idx", _I32, (t, routing.k), dev)
+    dw = None if d_topk_w is None else _arg(d_topk_w, "d_topk_w", _F32, (t, routing.k), dev)
+    c = None if counts is None else _arg(counts, "counts", _I32, (e + 1,), dev)
+    dl = None if d_losses is None else _arg(d_losses, "d_losses", _F32, (2,), dev)
+    mask = _token_mask(token_mask, t, dev)
+    with _On(dev, stream) as st:
+        out = torch.empty((t, e), dtype=logits.dtype, device=dev)
+        _check(lib().moe_route_backward(args, logits.data_ptr(), idx, dw, c, dl, mask,
+                                        out.data_ptr(), st))
+    return out
