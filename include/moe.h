@@ -520,6 +520,62 @@ moe_status_t moe_route_backward(const moe_routing_t* routing, const void* logits
                                 const int32_t* counts, const float* d_losses,
                                 const uint8_t* token_mask, void* d_logits, moe_stream_t stream);
 
+/* Gradient of moe_combine (the residual's is d_out itself):
+ *   dy_perm[row_of[t,j]] = topk_w[t,j] * d_out[t]   (fp32; one rounding)
+ *   d_topk_w[t,j]        = sum_h d_out[t,h] * y_perm[row_of[t,j],h]   (fp32 sum)
+ * and zero in every row of dy_perm that no slot names: the groups' pad rows and the rows
+ * past the last group.
+ *   d_out [T, hidden] bf16; y_perm [num_rows, hidden] fp32; row_of [T, k] int32, distinct
+ *   rows (a row outside [0, num_rows) is no slot: nothing is written for it and its
+ *   d_topk_w is 0); topk_w [T, k] fp32; expert_counts [E] and expert_offsets [E + 1] int32 as
+ *   moe_permute writes them: group e's routed rows start at offsets[e];
+ *   dy_perm [num_rows, hidden] fp32 out, nullable (then topk_w, expert_counts and
+ *   expert_offsets are not read and may be NULL); d_topk_w [T, k] fp32 out, nullable (then
+ *   y_perm is not read and may be NULL).
+ *   num_tokens >= 0, 1 <= k <= 8, hidden a positive multiple of 8, 1 <= num_experts <= 512,
+ *   num_rows >= 0. */
+moe_status_t moe_combine_backward(const moe_bf16_t* d_out, const float* y_perm,
+                                  const int32_t* row_of, const float* topk_w,
+                                  const int32_t* expert_counts, const int32_t* expert_offsets,
+                                  float* dy_perm, float* d_topk_w, int64_t num_tokens, int k,
+                                  int hidden, int num_experts, int64_t num_rows,
+                                  moe_stream_t stream);
+
+/* ---- Low-rank adapters of many requests beside a shared projection ----
+ * out[r] = base[r] + scale[g] * ((x[r] a[g]^T) b[g]^T),  g = adapter[r]
+ * for rows r of many requests, each with an adapter of its own or none: base is the shared
+ * projection's output, x its input. A row whose adapter is outside [0, num_adapters) (-1
+ * by convention) has none: out[r] = base[r].
+ *   x [R, in_features] bf16; a [G, rank, in_features] bf16; b [G, out_features, rank] bf16;
+ *   scale [G] fp32, nullable (1); adapter [R] int32; base and out [R, out_features], both
+ *   fp32 (out_fp32 = 1) or bf16 (0). out may be base itself (the same pointer and stride);
+ *   otherwise it overlaps no input. An adapter of smaller rank is padded with zeros.
+ *   Sums are fp32; the rank-wide intermediate stays fp32 (or is carried in parts that
+ *   together hold at least 16 bits of it for bf16 outputs and 24 for fp32 ones); out is
+ *   rounded once.
+ *   num_rows >= 0; in_features and out_features positive multiples of 8; rank a multiple of
+ *   8 in [8, 128]; 1 <= num_adapters <= 16384; the strides (elements from one row to the next)
+ *   multiples of 8, at least the row's length; x, a, b, base and out 16-byte aligned.
+ *   ws: a device workspace of moe_lora_workspace() bytes (256-byte aligned; its content
+ *   does not matter). */
+typedef struct {
+  int64_t num_rows;
+  int64_t x_stride;
+  int64_t base_stride;
+  int64_t out_stride;
+  int32_t in_features;
+  int32_t out_features;
+  int32_t rank;
+  int32_t num_adapters;
+  int32_t out_fp32;
+} moe_lora_t;
+
+size_t moe_lora_workspace(const moe_lora_t* lora);
+moe_status_t moe_lora_add(const moe_lora_t* lora, const void* base, const moe_bf16_t* x,
+                          const moe_bf16_t* a, const moe_bf16_t* b, const int32_t* adapter,
+                          const float* scale, void* out, void* ws, size_t ws_bytes,
+                          moe_stream_t stream);
+
 /* Waits for `stream`, then reads and clears the device status word in `ws`:
  * MOE_OK, or MOE_ERR_TIMEOUT if a kernel gave up a bounded wait since the last
  * call. */

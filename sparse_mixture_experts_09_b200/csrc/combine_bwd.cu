@@ -1,0 +1,132 @@
+// Gradient of the weighted combine in the expert rows and the routing weights.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxExperts = 512;
+
+// Rows that no slot names: group e's pads are [offsets[e] + counts[e], offsets[e + 1]),
+// the rows past the last group [offsets[E], rows). The block's threads zero every
+// `stride`-th of them, counting from `first`.
+__device__ void zero_unnamed(const CombineBwd& c, int64_t first, int64_t stride) {
+  __shared__ int32_t s_start[kMaxExperts + 1], s_count[kMaxExperts + 1];
+  for (int e = threadIdx.x; e <= c.E; e += kThreads) {
+    const int64_t lo = e < c.E ? (int64_t)c.offsets[e] + c.counts[e] : c.offsets[c.E];
+    const int64_t hi = e < c.E ? (int64_t)c.offsets[e + 1] : c.rows;
+    const int64_t a = lo < 0 ? 0 : lo, b = hi > c.rows ? c.rows : hi;
+    s_start[e] = (int32_t)a;
+    s_count[e] = b > a ? (int32_t)(b - a) : 0;
+  }
+  __syncthreads();
+  int64_t before = 0;  // unnamed rows before segment e
+  int64_t next = first;
+  const int vecs = c.H >> 2;
+  for (int e = 0; e <= c.E; ++e) {
+    for (; next < before + s_count[e]; next += stride) {
+      float4* row = reinterpret_cast<float4*>(c.dy + (s_start[e] + (next - before)) * (int64_t)c.H);
+      for (int i = threadIdx.x; i < vecs; i += kThreads) row[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    before += s_count[e];
+  }
+}
+
+// Blocks [0, token_blocks) take a token each (striding); the others zero the rows that
+// no slot names. A token's d_out is read once for its k rows; a thread adds its products
+// in fp32, then the warp and the block add in a fixed order. Bound by HBM: 2 H bytes of
+// d_out and 8 H of every routed row.
+template <int K>
+__global__ void __launch_bounds__(kThreads) k_combine_bwd(const CombineBwd c, int token_blocks) {
+  pdl_trigger();
+  pdl_wait();
+  if ((int)blockIdx.x >= token_blocks) {
+    zero_unnamed(c, (int64_t)blockIdx.x - token_blocks, (int64_t)gridDim.x - token_blocks);
+    return;
+  }
+  __shared__ float s_sum[K][kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int vecs = c.H >> 3;
+  for (int64_t t = blockIdx.x; t < c.T; t += token_blocks) {
+    int64_t row[K];
+    float w[K], sum[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      row[j] = j < c.k ? c.row_of[t * c.k + j] : -1;
+      if (row[j] >= c.rows) row[j] = -1;
+      w[j] = c.dy && row[j] >= 0 ? c.w[t * c.k + j] : 0.f;
+      sum[j] = 0.f;
+    }
+    for (int i = threadIdx.x; i < vecs; i += kThreads) {
+      const uint4 d = __ldg(reinterpret_cast<const uint4*>(c.d_out + t * c.H) + i);
+      float4 y[K][2];
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        if (c.d_w && row[j] >= 0) {
+          const float4* p = reinterpret_cast<const float4*>(c.y + row[j] * c.H) + 2 * i;
+          y[j][0] = __ldcs(p);
+          y[j][1] = __ldcs(p + 1);
+        }
+      }
+      const uint32_t q[4] = {d.x, d.y, d.z, d.w};
+      float g[8];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        g[2 * n] = __uint_as_float(q[n] << 16);
+        g[2 * n + 1] = __uint_as_float(q[n] & 0xFFFF0000u);
+      }
+#pragma unroll
+      for (int j = 0; j < K; ++j) {
+        if (row[j] < 0) continue;
+        if (c.d_w) {
+          const float v[8] = {y[j][0].x, y[j][0].y, y[j][0].z, y[j][0].w,
+                              y[j][1].x, y[j][1].y, y[j][1].z, y[j][1].w};
+#pragma unroll
+          for (int n = 0; n < 8; ++n) sum[j] = fmaf(g[n], v[n], sum[j]);
+        }
+        if (c.dy) {
+          float4* p = reinterpret_cast<float4*>(c.dy + row[j] * c.H) + 2 * i;
+          __stcs(p, make_float4(w[j] * g[0], w[j] * g[1], w[j] * g[2], w[j] * g[3]));
+          __stcs(p + 1, make_float4(w[j] * g[4], w[j] * g[5], w[j] * g[6], w[j] * g[7]));
+        }
+      }
+    }
+    if (!c.d_w) continue;
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
+      if (lane == 0) s_sum[j][warp] = sum[j];
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < c.k) {
+      float all = 0.f;
+#pragma unroll
+      for (int v = 0; v < kThreads / 32; ++v) all += s_sum[threadIdx.x][v];
+      c.d_w[t * c.k + threadIdx.x] = all;
+    }
+    __syncthreads();
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_combine_bwd(const CombineBwd& c, cudaStream_t st) {
+  const int64_t cap = (int64_t)num_sms() * 8;
+  const int token_blocks = (int)(c.T < 4 * cap ? c.T : 4 * cap);
+  // T * k of `rows` rows are named; the rest bounds the zeroing blocks
+  int64_t zero_blocks = c.dy ? c.rows - c.T * c.k : 0;
+  if (zero_blocks > cap) zero_blocks = cap;
+  if (c.dy && c.rows > 0 && zero_blocks < 1) zero_blocks = 1;  // slots may name no row
+  const int64_t blocks = token_blocks + zero_blocks;
+  if (blocks == 0) return cudaSuccess;
+  const dim3 grid((unsigned)blocks), block(kThreads);
+  if (c.k <= 2) return launch_pdl(k_combine_bwd<2>, grid, block, 0, st, c, token_blocks);
+  if (c.k <= 4) return launch_pdl(k_combine_bwd<4>, grid, block, 0, st, c, token_blocks);
+  return launch_pdl(k_combine_bwd<8>, grid, block, 0, st, c, token_blocks);
+}
+
+}  // namespace moe

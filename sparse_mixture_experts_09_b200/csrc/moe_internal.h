@@ -200,6 +200,37 @@ cudaError_t launch_route_backward(const Routing& r, const void* logits, const in
                                   const float* d_w, const int32_t* counts, const float* d_losses,
                                   const uint8_t* mask, void* d_logits, cudaStream_t st);
 
+// Gradient of the combine (combine_bwd.cu).
+struct CombineBwd {
+  const uint16_t* d_out;
+  const float* y;
+  const int32_t* row_of;
+  const float* w;
+  const int32_t* counts;
+  const int32_t* offsets;
+  float* dy;
+  float* d_w;
+  int64_t T, rows;
+  int k, H, E;
+};
+cudaError_t launch_combine_bwd(const CombineBwd& c, cudaStream_t st);
+
+// Low-rank adapters beside a shared projection (lora.cu).
+struct Lora {
+  int64_t R, x_stride, base_stride, out_stride;
+  int H, N, rank, G;
+  int fp32;
+  const uint16_t* x;
+  const uint16_t* a;
+  const uint16_t* b;
+  const int32_t* adapter;
+  const float* scale;
+  const void* base;
+  void* out;
+};
+size_t lora_workspace(const Lora& l);
+cudaError_t launch_lora(const Lora& l, void* ws, cudaStream_t st);
+
 int num_sms();
 
 // Host helpers of the C ABI (moe_api.cu): shape validation returning a moe_status_t
@@ -207,7 +238,7 @@ int num_sms();
 int validate_shape(const moe_shape_t* shape, Shape* out);
 void set_error_message(const char* msg);
 
-// Checks shared by the entry points outside moe_api.cu (route_api.cu): a status with its
+// Checks shared by the entry points outside moe_api.cu (router_adapter_api.cu): a status with its
 // message, a launch's result, and a pointer's presence and alignment.
 moe_status_t fail_with(moe_status_t code, const char* fmt, ...);
 moe_status_t launched(cudaError_t e, const char* where);

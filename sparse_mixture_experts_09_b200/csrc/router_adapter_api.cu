@@ -1,7 +1,8 @@
-// C ABI of the general routing, the router losses and their gradient: argument checks and
-// launches. Contracts are in include/moe.h.
+// C ABI of the general routing, the router losses, the gradients and the low-rank adapters:
+// argument checks and launches. Contracts are in include/moe.h.
 #include <cuda_runtime.h>
 #include <math.h>
+#include <limits.h>
 #include <stdarg.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -115,6 +116,39 @@ LossLayout loss_layout(const Routing& r) {
   return l;
 }
 
+moe_status_t check_lora(const moe_lora_t* in, Lora* out) {
+  if (!in) return fail_with(MOE_ERR_INVALID_ARG, "lora is NULL");
+  if (in->num_rows < 0 || in->num_rows > 1 << 24)
+    return fail_with(MOE_ERR_INVALID_ARG, "num_rows must be in [0, 2^24] (got %lld)",
+                     (long long)in->num_rows);
+  if (in->in_features <= 0 || in->in_features % 8 || in->out_features <= 0 || in->out_features % 8 ||
+      in->in_features > 1 << 20 || in->out_features > 1 << 20)
+    return fail_with(MOE_ERR_UNSUPPORTED,
+                     "in_features and out_features must be positive multiples of 8, at most 2^20 "
+                     "(got %d and %d)", in->in_features, in->out_features);
+  if (in->rank < 8 || in->rank > 128 || in->rank % 8)
+    return fail_with(MOE_ERR_UNSUPPORTED, "rank must be a multiple of 8 in [8, 128] (got %d)", in->rank);
+  if (in->num_adapters < 1 || in->num_adapters > 16384)
+    return fail_with(MOE_ERR_UNSUPPORTED, "num_adapters must be in [1, 16384] (got %d)",
+                     in->num_adapters);
+  if (in->x_stride < in->in_features || in->x_stride % 8 || in->base_stride < in->out_features ||
+      in->base_stride % 8 || in->out_stride < in->out_features || in->out_stride % 8)
+    return fail_with(MOE_ERR_INVALID_ARG,
+                     "the row strides must be multiples of 8, at least the row's length");
+  if (in->out_fp32 != 0 && in->out_fp32 != 1)
+    return fail_with(MOE_ERR_INVALID_ARG, "out_fp32 must be 0 or 1 (got %d)", in->out_fp32);
+  out->R = in->num_rows;
+  out->x_stride = in->x_stride;
+  out->base_stride = in->base_stride;
+  out->out_stride = in->out_stride;
+  out->H = in->in_features;
+  out->N = in->out_features;
+  out->rank = in->rank;
+  out->G = in->num_adapters;
+  out->fp32 = in->out_fp32;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -184,6 +218,88 @@ moe_status_t moe_route_backward(const moe_routing_t* routing, const void* logits
   return launched(launch_route_backward(r, logits, topk_idx, d_topk_w, counts, d_losses, token_mask,
                                         d_logits, (cudaStream_t)stream),
                   "routing backward launch");
+}
+
+moe_status_t moe_combine_backward(const moe_bf16_t* d_out, const float* y_perm,
+                                  const int32_t* row_of, const float* topk_w,
+                                  const int32_t* expert_counts, const int32_t* expert_offsets,
+                                  float* dy_perm, float* d_topk_w, int64_t num_tokens, int k,
+                                  int hidden, int num_experts, int64_t num_rows,
+                                  moe_stream_t stream) {
+  set_error_message("");
+  if (num_tokens < 0 || num_rows < 0 || num_rows > INT_MAX)
+    return fail_with(MOE_ERR_INVALID_ARG, "num_tokens and num_rows must be in [0, 2^31)");
+  if (k < 1 || k > 8) return fail_with(MOE_ERR_UNSUPPORTED, "k must be in [1, 8] (got %d)", k);
+  if (num_tokens > ((int64_t)1 << 30) / k)
+    return fail_with(MOE_ERR_UNSUPPORTED, "num_tokens * k must be <= 2^30");
+  if (hidden <= 0 || hidden % 8)
+    return fail_with(MOE_ERR_UNSUPPORTED, "hidden must be a positive multiple of 8 (got %d)", hidden);
+  if (num_experts < 1 || num_experts > 512)
+    return fail_with(MOE_ERR_UNSUPPORTED, "num_experts must be in [1, 512] (got %d)", num_experts);
+  const bool none = num_tokens == 0;
+  MOE_TRY(check_aligned(d_out, "d_out", 16, none));
+  MOE_TRY(check_aligned(row_of, "row_of", 4, none));
+  MOE_TRY(check_aligned(dy_perm, "dy_perm", 16, true));
+  MOE_TRY(check_aligned(d_topk_w, "d_topk_w", 4, true));
+  MOE_TRY(check_aligned(y_perm, "y_perm", 16, none || !d_topk_w || num_rows == 0));
+  MOE_TRY(check_aligned(topk_w, "topk_w", 4, none || !dy_perm));
+  MOE_TRY(check_aligned(expert_counts, "expert_counts", 4, !dy_perm));
+  MOE_TRY(check_aligned(expert_offsets, "expert_offsets", 4, !dy_perm));
+  if (!dy_perm && !d_topk_w) return MOE_OK;
+  CombineBwd c;
+  c.d_out = d_out;
+  c.y = y_perm;
+  c.row_of = row_of;
+  c.w = topk_w;
+  c.counts = expert_counts;
+  c.offsets = expert_offsets;
+  c.dy = dy_perm;
+  c.d_w = d_topk_w;
+  c.T = num_tokens;
+  c.rows = num_rows;
+  c.k = k;
+  c.H = hidden;
+  c.E = num_experts;
+  return launched(launch_combine_bwd(c, (cudaStream_t)stream), "combine backward launch");
+}
+
+size_t moe_lora_workspace(const moe_lora_t* lora) {
+  set_error_message("");
+  Lora l = {};
+  if (check_lora(lora, &l) != MOE_OK) return 0;
+  return lora_workspace(l);
+}
+
+moe_status_t moe_lora_add(const moe_lora_t* lora, const void* base, const moe_bf16_t* x,
+                          const moe_bf16_t* a, const moe_bf16_t* b, const int32_t* adapter,
+                          const float* scale, void* out, void* ws, size_t ws_bytes,
+                          moe_stream_t stream) {
+  set_error_message("");
+  Lora l = {};
+  MOE_TRY(check_lora(lora, &l));
+  if (l.R == 0) return MOE_OK;
+  MOE_TRY(check_aligned(base, "base", 16, false));
+  MOE_TRY(check_aligned(x, "x", 16, false));
+  MOE_TRY(check_aligned(a, "a", 16, false));
+  MOE_TRY(check_aligned(b, "b", 16, false));
+  MOE_TRY(check_aligned(adapter, "adapter", 4, false));
+  MOE_TRY(check_aligned(scale, "scale", 4, true));
+  MOE_TRY(check_aligned(out, "out", 16, false));
+  if (out == base && l.out_stride != l.base_stride)
+    return fail_with(MOE_ERR_INVALID_ARG, "out is base, but their strides differ");
+  const size_t need = lora_workspace(l);
+  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256)
+    return fail_with(MOE_ERR_WORKSPACE, "workspace is NULL or not 256-byte aligned");
+  if (ws_bytes < need)
+    return fail_with(MOE_ERR_WORKSPACE, "workspace too small: need %zu bytes, got %zu", need, ws_bytes);
+  l.x = x;
+  l.a = a;
+  l.b = b;
+  l.adapter = adapter;
+  l.scale = scale;
+  l.base = base;
+  l.out = out;
+  return launched(launch_lora(l, ws, (cudaStream_t)stream), "adapter launch");
 }
 
 }  // extern "C"

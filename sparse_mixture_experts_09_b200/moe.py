@@ -31,7 +31,8 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_size_host", "moe_max_padded_rows
            "moe_forward_host_async", "moe_quantize_int4", "moe_grouped_swiglu_w4", "moe_forward_w4",
            "moe_ipc_alloc", "moe_ipc_open", "moe_ipc_close", "moe_ipc_free",
            "moe_scatter_rows_peer", "moe_combine_peer", "moe_route", "moe_router_losses",
-           "moe_router_losses_workspace", "moe_route_backward")
+           "moe_router_losses_workspace", "moe_route_backward", "moe_combine_backward",
+           "moe_lora_workspace", "moe_lora_add")
 
 
 @dataclass
@@ -95,6 +96,14 @@ class _RoutingArgs(ctypes.Structure):
                 ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
                 ("renormalize", ctypes.c_int32), ("logits_bf16", ctypes.c_int32),
                 ("weight_scale", ctypes.c_float)]
+
+
+class _LoraArgs(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("base_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("rank", ctypes.c_int32), ("num_adapters", ctypes.c_int32),
+                ("out_fp32", ctypes.c_int32)]
 
 
 _lib = None
@@ -184,6 +193,14 @@ def lib() -> ctypes.CDLL:
         L.moe_router_losses.restype = st
         L.moe_route_backward.argtypes = [rp, _P, _P, _P, _P, _P, _P, _P, _P]
         L.moe_route_backward.restype = st
+        L.moe_combine_backward.argtypes = [_P] * 8 + [ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                                      ctypes.c_int, ctypes.c_int64, _P]
+        L.moe_combine_backward.restype = st
+        lp = ctypes.POINTER(_LoraArgs)
+        L.moe_lora_workspace.argtypes = [lp]
+        L.moe_lora_workspace.restype = _SZ
+        L.moe_lora_add.argtypes = [lp] + [_P] * 8 + [_SZ, _P]
+        L.moe_lora_add.restype = st
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -876,4 +893,79 @@ def route_backward(logits, topk_idx, routing: Routing, d_topk_w=None, counts=Non
         out = torch.empty((t, e), dtype=logits.dtype, device=dev)
         _check(lib().moe_route_backward(args, logits.data_ptr(), idx, dw, c, dl, mask,
                                         out.data_ptr(), st))
+    return out
+
+
+def combine_backward(d_out, y_perm, row_of, topk_w, counts=None, offsets=None, need_dy: bool = True,
+                     need_dw: bool = True, stream=None):
+    """(dy_perm, d_topk_w): gradient of combine for d_out [T, H] bf16 (see
+    moe_combine_backward). dy_perm is fp32 like y_perm [rows, H], zero in the rows no slot
+    names; counts [E] and offsets [E + 1] are permute's. need_dy=False or need_dw=False
+    leaves that one out (None); counts and offsets are needed for dy_perm only."""
+    if d_out.dim() != 2 or row_of.dim() != 2 or y_perm.dim() != 2:
+        raise ValueError("d_out, y_perm and row_of must be 2-D")
+    t, h = d_out.shape
+    k, rows = row_of.shape[1], y_perm.shape[0]
+    dev = d_out.device
+    d = _arg(d_out, "d_out", (torch.bfloat16,), (t, h))
+    y = _arg(y_perm, "y_perm", _F32, (rows, h), dev)
+    r = _arg(row_of, "row_of", _I32, (t, k), dev)
+    w = _arg(topk_w, "topk_w", _F32, (t, k), dev)
+    e, c, o = 1, None, None
+    if need_dy:
+        if counts is None or offsets is None:
+            raise ValueError("counts and offsets are required for dy_perm")
+        e = counts.numel()
+        c = _arg(counts, "counts", _I32, (e,), dev)
+        o = _arg(offsets, "offsets", _I32, (e + 1,), dev)
+    with _On(dev, stream) as st:
+        dy = torch.empty((rows, h), dtype=torch.float32, device=dev) if need_dy else None
+        dw = torch.empty((t, k), dtype=torch.float32, device=dev) if need_dw else None
+        _check(lib().moe_combine_backward(d, y, r, w, c, o, dy.data_ptr() if need_dy else None,
+                                          dw.data_ptr() if need_dw else None, t, k, h, e, rows, st))
+    return dy, dw
+
+
+# ---- low-rank adapters of many requests beside a shared projection ----
+
+def _rows(t, name: str, dtypes, shape, device=None):
+    """(address, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous along its rows")
+    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else shape[1])
+
+
+def lora_add(base, x, a, b, adapter, scale=None, out=None, stream=None):
+    """base + scale[g] * (x a[g]^T) b[g]^T per row, g = adapter[row] (int32; a value outside
+    [0, G) is a row without an adapter): base [R, N] bf16 or fp32, x [R, H] bf16, a [G, rank, H]
+    and b [G, N, rank] bf16, scale [G] fp32 or None. Rows of base, x and out may be strided.
+    Writes `out` when given (base itself: in place), else a new tensor (see moe_lora_add)."""
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [rows, in], a [adapters, rank, in], b [adapters, out, rank]")
+    r, h = x.shape
+    ad, rank, _ = a.shape
+    n = b.shape[1]
+    dev = x.device
+    xp, xs = _rows(x, "x", (torch.bfloat16,), (r, h))
+    ap = _arg(a, "a", (torch.bfloat16,), (ad, rank, h), dev)
+    bp = _arg(b, "b", (torch.bfloat16,), (ad, n, rank), dev)
+    ip = _arg(adapter, "adapter", _I32, (r,), dev)
+    sp = None if scale is None else _arg(scale, "scale", _F32, (ad,), dev)
+    base_p, base_s = _rows(base, "base", _LOGITS, (r, n), dev)
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty((r, n), dtype=base.dtype, device=dev)
+        out_p, out_s = _rows(out, "out", (base.dtype,), (r, n), dev)
+        args = _LoraArgs(r, xs, base_s, out_s, h, n, rank, ad, int(base.dtype == torch.float32))
+        size = lib().moe_lora_workspace(args)
+        ws = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
+        _check(lib().moe_lora_add(args, base_p, xp, ap, bp, ip, sp, out_p, ws.data_ptr(), size, st))
     return out
