@@ -154,11 +154,491 @@ cudaError_t expand_rows(const Lora& l, const float* t, cudaStream_t st) {
   return launch_pdl(k_expand_rows<T, 16>, grid, block, 0, st, l, t, blocks_per_row);
 }
 
+// ---- many rows: tiles of up to 64 rows of one adapter on the matrix pipe ----
+//
+// Three launches. k_plan sorts the rows by adapter and cuts each adapter's rows into
+// tiles. k_shrink_tiles forms x a^T per tile and slice of the features (slices keep the
+// GPU busy when there are few tiles). k_expand_tiles adds the slices up, and streams base
+// to out with t b^T on the way. Rows are independent in a matrix product and every sum's
+// order is fixed by the sizes, so the order within a tile does not show in the result.
+//
+// The work is bound by HBM: out and base at 2 or 4 bytes an element against 2 * rank
+// operations (times the parts of t, below), so mma.sync, whose fragments feed straight
+// from shared memory and whose sums lie in the registers that hold base, is fast enough
+// and a tensor-memory pipeline would have nothing to hide.
+
+constexpr int kTileRows = 64;
+constexpr int kChunkK = 64;    // features per stage of the shrink
+constexpr int kStages = 4;     // of the shrink
+constexpr int kChunkN = 128;   // columns per step of the expand
+
+// In the workspace: the tiles {adapter or -1, first sorted row, rows, 0}, their count, the
+// sorted row numbers, and the shrink's sums [slices][R][RP].
+struct Plan {
+  int4* tiles;
+  int32_t* count;
+  int32_t* order;
+  float* part;
+};
+
+__host__ __device__ inline int64_t max_tiles(int64_t R, int G) {
+  const int64_t groups = G + 1 < R ? G + 1 : R;
+  return (R + kTileRows - 1) / kTileRows + groups;
+}
+
+// Counting sort of the rows by adapter, one block: rows without an adapter form group G.
+// Lanes of a warp with the same adapter add once (runs of a request are the common case).
+__global__ void __launch_bounds__(1024) k_plan(const Lora l, Plan p) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ int32_t s_cursor[];  // [G + 1] counts, then each group's next position
+  __shared__ int32_t s_rows[32], s_tiles[32];
+  const int groups = l.G + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int g = threadIdx.x; g < groups; g += 1024) s_cursor[g] = 0;
+  __syncthreads();
+  const int64_t rounds = (l.R + 1023) / 1024;
+  for (int64_t i = 0; i < rounds; ++i) {
+    const int64_t r = i * 1024 + threadIdx.x;
+    const int g = r < l.R ? (adapter_of(l, r) < 0 ? l.G : l.adapter[r]) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, g);
+    if (g >= 0 && lane == __ffs(same) - 1) atomicAdd(&s_cursor[g], __popc(same));
+  }
+  __syncthreads();
+  // exclusive prefixes of rows and tiles over the groups: `per` neighbouring groups a thread
+  const int per = (groups + 1023) / 1024;
+  const int g0 = threadIdx.x * per, g1 = g0 + per < groups ? g0 + per : groups;
+  int rows = 0, tiles = 0;
+  for (int g = g0; g < g1; ++g) {
+    rows += s_cursor[g];
+    tiles += (s_cursor[g] + kTileRows - 1) / kTileRows;
+  }
+  int row_at = rows, tile_at = tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, row_at, o);
+    const int b = __shfl_up_sync(0xffffffffu, tile_at, o);
+    if (lane >= o) {
+      row_at += a;
+      tile_at += b;
+    }
+  }
+  if (lane == 31) {
+    s_rows[warp] = row_at;
+    s_tiles[warp] = tile_at;
+  }
+  __syncthreads();
+  int row_base = 0, tile_base = 0;
+  for (int w = 0; w < warp; ++w) {
+    row_base += s_rows[w];
+    tile_base += s_tiles[w];
+  }
+  row_at += row_base - rows;
+  tile_at += tile_base - tiles;
+  if (threadIdx.x == 1023) *p.count = tile_at + tiles;
+  for (int g = g0; g < g1; ++g) {
+    const int n = s_cursor[g];
+    s_cursor[g] = row_at;
+    for (int i = 0; i < n; i += kTileRows)
+      p.tiles[tile_at++] = make_int4(g < l.G ? g : -1, row_at + i, n - i < kTileRows ? n - i : kTileRows, 0);
+    row_at += n;
+  }
+  __syncthreads();
+  for (int64_t i = 0; i < rounds; ++i) {
+    const int64_t r = i * 1024 + threadIdx.x;
+    const int g = r < l.R ? (adapter_of(l, r) < 0 ? l.G : l.adapter[r]) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, g);
+    int at = 0;
+    if (g >= 0 && lane == __ffs(same) - 1) at = atomicAdd(&s_cursor[g], __popc(same));
+    at = __shfl_sync(0xffffffffu, at, __ffs(same) - 1);
+    if (g >= 0) p.order[at + __popc(same & ((1u << lane) - 1u))] = (int32_t)r;
+  }
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+// 16 bytes from global to shared memory; zeros when !in (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// One tile and slice of the features: 4 warps of 16 rows each by RP ranks (RP: rank rounded up
+// to 16, 32, 64 or 128). x and a come in stages of 64 features by 16-byte asynchronous
+// copies, their 16-byte pieces swizzled by the row. The matrix pipe's own sums are
+// truncated, not rounded, at each step, so they run over one stage only (4 steps) and are
+// added to the running sums by ordinary additions.
+template <int RP>
+__global__ void __launch_bounds__(128) k_shrink_tiles(const Lora l, const Plan p, int slices) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kStageBytes = (kTileRows + RP) * kChunkK * 2;
+  const int tile = blockIdx.x / slices, slice = blockIdx.x - tile * slices;
+  if (tile >= *p.count) return;
+  const int4 tl = p.tiles[tile];
+  if (tl.x < 0) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunks = (l.H + kChunkK - 1) / kChunkK, per = (chunks + slices - 1) / slices;
+  const int c0 = slice * per, c1 = c0 + per < chunks ? c0 + per : chunks;
+  // this thread's pieces: column piece tid % 8 of rows tid / 8 + 16 i
+  const int piece = tid & 7, row0 = tid >> 3;
+  const uint16_t* xs[kTileRows / 16];
+  bool x_in[kTileRows / 16];
+#pragma unroll
+  for (int i = 0; i < kTileRows / 16; ++i) {
+    const int r = row0 + 16 * i;
+    x_in[i] = r < tl.z;
+    xs[i] = l.x + (x_in[i] ? (int64_t)p.order[tl.y + r] * l.x_stride : 0);
+  }
+  const uint16_t* as = l.a + (int64_t)tl.x * l.rank * l.H;
+  const uint32_t base = smem_addr(smem);
+  auto load = [&](int c, int stage) {
+    const int col = c * kChunkK + piece * 8;
+    const bool in = c < c1 && col < l.H;
+    const uint32_t st = base + stage * kStageBytes;
+#pragma unroll
+    for (int i = 0; i < kTileRows / 16; ++i) {
+      const int r = row0 + 16 * i;
+      const bool ok = in && x_in[i];
+      copy16(st + r * 128 + ((piece ^ (r & 7)) << 4), ok ? xs[i] + col : l.x, ok);
+    }
+#pragma unroll
+    for (int i = 0; i < RP / 16; ++i) {
+      const int r = row0 + 16 * i;
+      const bool ok = in && r < l.rank;
+      copy16(st + (kTileRows + r) * 128 + ((piece ^ (r & 7)) << 4),
+             ok ? as + (int64_t)r * l.H + col : l.a, ok);
+    }
+    copies_end();
+  };
+  float sum[RP / 8][4];
+#pragma unroll
+  for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[n][i] = 0.f;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) load(c0 + s, s);
+  for (int c = c0; c < c1; ++c) {
+    copies_wait<kStages - 2>();
+    __syncthreads();
+    load(c + kStages - 1, (c - c0 + kStages - 1) % kStages);
+    const uint32_t xt = base + ((c - c0) % kStages) * kStageBytes, at = xt + kTileRows * 128;
+    float acc[RP / 8][4];
+#pragma unroll
+    for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < kChunkK / 16; ++kk) {
+      uint32_t xf[4];
+      const int xr = warp * 16 + (lane & 15);
+      ldsm4(xf, xt + xr * 128 + (((kk * 2 + (lane >> 4)) ^ (xr & 7)) << 4));
+#pragma unroll
+      for (int n = 0; n < RP / 16; ++n) {
+        uint32_t bf[4];
+        const int ar = n * 16 + (lane & 7) + ((lane >> 4) << 3);
+        ldsm4(bf, at + ar * 128 + (((kk * 2 + ((lane >> 3) & 1)) ^ (ar & 7)) << 4));
+        mma(acc[2 * n], xf, bf[0], bf[1]);
+        mma(acc[2 * n + 1], xf, bf[2], bf[3]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < RP / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[n][i] += acc[n][i];
+  }
+  copies_wait<0>();
+  float* out = p.part + (int64_t)slice * l.R * RP;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = warp * 16 + (lane >> 2) + 8 * h;
+    if (r >= tl.z) continue;
+    float2* o = reinterpret_cast<float2*>(out + (int64_t)(tl.y + r) * RP + (lane & 3) * 2);
+#pragma unroll
+    for (int n = 0; n < RP / 8; ++n) o[n * 4] = make_float2(sum[n][2 * h], sum[n][2 * h + 1]);
+  }
+}
+
+// Sixteen bytes of the output in floats, and back (one rounding for bf16).
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static __device__ void get(const uint4& v, float (&f)[4]) {
+    f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+  }
+  static __device__ uint4 put(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+};
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ void get(const uint4& v, float (&f)[8]) {
+    f[0] = lo(v.x), f[1] = hi(v.x), f[2] = lo(v.y), f[3] = hi(v.y);
+    f[4] = lo(v.z), f[5] = hi(v.z), f[6] = lo(v.w), f[7] = hi(v.w);
+  }
+  static __device__ uint4 put(const float (&f)[8]) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+  }
+};
+
+// One tile and a run of columns, 128 columns a step: 8 warps as 4 (16 rows) x 2 (64 columns).
+// t (the slices' sum, times the scale) is cut into bf16 parts whose sum holds it to 2^-24
+// (3 parts, fp32 out) or 2^-16 (2 parts, bf16 out: far below its one rounding), so the
+// products with b are exact in fp32. b's rows of a step go to shared memory in the order
+// in which a thread's columns of neighbouring 8-wide products are neighbours in out:
+// base is read and out is written 16 bytes at a time straight from the registers.
+template <typename T, int RP>
+__global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1)
+    k_expand_tiles(const Lora l, const Plan p, int slices, int col_runs, int steps_per_run) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kParts = sizeof(T) == 4 ? 3 : 2;
+  constexpr int kPitch = RP * 2 + 16;  // odd in 16-byte units: ldmatrix rows fall on distinct banks
+  constexpr int kVec = Vec<T>::kN;     // columns of one 16-byte access
+  constexpr int kWide = kVec / 2;      // 8-wide products that share it
+  const int tile = blockIdx.x / col_runs, run = blockIdx.x - tile * col_runs;
+  if (tile >= *p.count) return;
+  const int4 tl = p.tiles[tile];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const T* base = static_cast<const T*>(l.base);
+  T* out = static_cast<T*>(l.out);
+  const int s0 = run * steps_per_run, steps = (l.N + kChunkN - 1) / kChunkN;
+  const int s1 = s0 + steps_per_run < steps ? s0 + steps_per_run : steps;
+  if (tl.x < 0) {  // rows without an adapter
+    if (l.base == l.out) return;
+    const int n0 = s0 * kChunkN, n1 = s1 * kChunkN < l.N ? s1 * kChunkN : l.N;
+    const int vecs = (n1 - n0) / kVec;
+    for (int i = tid; i < tl.z * vecs; i += 256) {
+      const int64_t r = p.order[tl.y + i / vecs];
+      const int n = n0 + i % vecs * kVec;
+      *reinterpret_cast<uint4*>(out + r * l.out_stride + n) =
+          *reinterpret_cast<const uint4*>(base + r * l.base_stride + n);
+    }
+    return;
+  }
+  const uint32_t t_at = smem_addr(smem), b_at = t_at + kParts * kTileRows * kPitch;
+  constexpr int kStepBytes = kChunkN * kPitch;
+  const uint16_t* bg = l.b + (int64_t)tl.x * l.N * l.rank;
+  auto load_b = [&](int s) {
+    constexpr int kPieces = RP / 8;
+    const uint32_t st = b_at + (s & 1) * kStepBytes;
+#pragma unroll
+    for (int i = 0; i < kChunkN * kPieces / 256; ++i) {
+      const int q = tid + 256 * i, n = q / kPieces, piece = q - n * kPieces;
+      const int col = s * kChunkN + n;
+      const bool in = s < s1 && col < l.N && piece * 8 < l.rank;
+      // column n = 8 kWide G + 2 kWide c + 2 w + e sits at row 8 kWide G + 8 w + 2 c + e
+      const int row = n / (8 * kWide) * (8 * kWide) + (n % (2 * kWide)) / 2 * 8 +
+                      (n % (8 * kWide)) / (2 * kWide) * 2 + (n & 1);
+      copy16(st + row * kPitch + piece * 16, in ? bg + (int64_t)col * l.rank + piece * 8 : l.b, in);
+    }
+    copies_end();
+  };
+  load_b(s0);
+  // t: the slices in order, the scale, the parts
+  const float scale = l.scale ? l.scale[tl.x] : 1.f;
+  for (int i = tid; i < kTileRows * RP / 2; i += 256) {
+    const int r = i / (RP / 2), c = (i - r * (RP / 2)) * 2;
+    float2 v = make_float2(0.f, 0.f);
+    if (r < tl.z) {
+      const float* src = p.part + (int64_t)(tl.y + r) * RP + c;
+      for (int s = 0; s < slices; ++s) {
+        const float2 q = *reinterpret_cast<const float2*>(src + (int64_t)s * l.R * RP);
+        v.x += q.x;
+        v.y += q.y;
+      }
+      v.x *= scale;
+      v.y *= scale;
+    }
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) {
+      const uint32_t both = pack2(v.x, v.y);
+      *reinterpret_cast<uint32_t*>(smem + (part * kTileRows + r) * kPitch + c * 2) = both;
+      v.x -= lo(both);
+      v.y -= hi(both);
+    }
+  }
+  const int wr = (warp & 3) * 16, wc = (warp >> 2) * 64;
+  const int r0 = wr + (lane >> 2), r1 = r0 + 8;
+  const bool in0 = r0 < tl.z, in1 = r1 < tl.z;
+  const int64_t g0 = in0 ? p.order[tl.y + r0] : 0, g1 = in1 ? p.order[tl.y + r1] : 0;
+  constexpr int kGroups = 64 / (8 * kWide);
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  for (int s = s0; s < s1; ++s) {
+    copies_wait<0>();
+    __syncthreads();
+    load_b(s + 1);
+    uint4 was[2][kGroups];
+    const int col0 = s * kChunkN + wc + (lane & 3) * kVec;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int col = col0 + g * 8 * kWide;
+      const bool in = col < l.N;
+      was[0][g] = in && in0 ? *reinterpret_cast<const uint4*>(base + g0 * l.base_stride + col) : zero;
+      was[1][g] = in && in1 ? *reinterpret_cast<const uint4*>(base + g1 * l.base_stride + col) : zero;
+    }
+    float acc[8][4];
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+    const uint32_t bt = b_at + (s & 1) * kStepBytes;
+#pragma unroll
+    for (int kk = 0; kk < RP / 16; ++kk) {
+      uint32_t tf[kParts][4];
+#pragma unroll
+      for (int part = 0; part < kParts; ++part)
+        ldsm4(tf[part], t_at + (part * kTileRows + wr + (lane & 15)) * kPitch + kk * 32 + (lane >> 4) * 16);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        uint32_t bf[4];
+        ldsm4(bf, bt + (wc + n * 16 + (lane & 7) + ((lane >> 4) << 3)) * kPitch + kk * 32 +
+                      ((lane >> 3) & 1) * 16);
+#pragma unroll
+        for (int part = kParts - 1; part >= 0; --part) {
+          mma(acc[2 * n], tf[part], bf[0], bf[1]);
+          mma(acc[2 * n + 1], tf[part], bf[2], bf[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      const int col = col0 + g * 8 * kWide;
+      if (col >= l.N) continue;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!(h ? in1 : in0)) continue;
+        float f[kVec];
+        Vec<T>::get(was[h][g], f);
+#pragma unroll
+        for (int w = 0; w < kWide; ++w) {
+          f[2 * w] += acc[g * kWide + w][2 * h];
+          f[2 * w + 1] += acc[g * kWide + w][2 * h + 1];
+        }
+        *reinterpret_cast<uint4*>(out + (h ? g1 : g0) * l.out_stride + col) = Vec<T>::put(f);
+      }
+    }
+  }
+  copies_wait<0>();
+}
+
+int rank_pad(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+
+// Rows from which the tiles are used.
+constexpr int64_t kTilesFrom = 128;
+
+// Slices of the features: enough blocks for four on every SM, at least two stages each.
+int feature_slices(const Lora& l) {
+  const int64_t tiles = (l.R + kTileRows - 1) / kTileRows;
+  const int64_t chunks = (l.H + kChunkK - 1) / kChunkK;
+  int64_t s = ((int64_t)num_sms() * 4 + tiles - 1) / tiles;
+  if (s > chunks / 2) s = chunks / 2;
+  return s < 1 ? 1 : s > 8 ? 8 : (int)s;
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+Plan plan_at(const Lora& l, void* ws, size_t* end) {
+  char* at = static_cast<char*>(ws);
+  Plan p;
+  p.count = reinterpret_cast<int32_t*>(at);
+  at += 256;
+  p.tiles = reinterpret_cast<int4*>(at);
+  at += up256((size_t)max_tiles(l.R, l.G) * 16);
+  p.order = reinterpret_cast<int32_t*>(at);
+  at += up256((size_t)l.R * 4);
+  p.part = reinterpret_cast<float*>(at);
+  at += up256((size_t)feature_slices(l) * l.R * rank_pad(l.rank) * 4);
+  *end = (size_t)(at - static_cast<char*>(ws));
+  return p;
+}
+
+// A block's shared memory above 48 KB has to be asked for (1 KB is left to static arrays).
+template <typename F>
+cudaError_t allow_smem(F* kernel, size_t bytes) {
+  if (bytes <= 47 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <int RP>
+cudaError_t run_tiles(const Lora& l, const Plan& p, cudaStream_t st) {
+  const int slices = feature_slices(l);
+  const int64_t tiles = max_tiles(l.R, l.G);
+  const size_t shrink_smem = (size_t)kStages * (kTileRows + RP) * kChunkK * 2;
+  cudaError_t e = allow_smem(k_shrink_tiles<RP>, shrink_smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k_shrink_tiles<RP>, dim3((unsigned)(tiles * slices)), dim3(128), shrink_smem, st, l,
+                 p, slices);
+  if (e != cudaSuccess) return e;
+  const int steps = (l.N + kChunkN - 1) / kChunkN;
+  const int per = steps < 8 ? steps : 8;
+  const int runs = (steps + per - 1) / per;
+  const int parts = l.fp32 ? 3 : 2;
+  const size_t smem = (size_t)(parts * kTileRows + 2 * kChunkN) * (RP * 2 + 16);
+  const dim3 grid((unsigned)(tiles * runs)), block(256);
+  if (l.fp32) {
+    e = allow_smem(k_expand_tiles<float, RP>, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_expand_tiles<float, RP>, grid, block, smem, st, l, p, slices, runs, per);
+  }
+  e = allow_smem(k_expand_tiles<__nv_bfloat16, RP>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_expand_tiles<__nv_bfloat16, RP>, grid, block, smem, st, l, p, slices, runs, per);
+}
+
 }  // namespace
 
-size_t lora_workspace(const Lora& l) { return ((size_t)l.R * l.rank * 4 + 255) / 256 * 256 + 256; }
+size_t lora_workspace(const Lora& l) {
+  if (l.R < kTilesFrom) return up256((size_t)l.R * l.rank * 4) + 256;
+  size_t end = 0;
+  plan_at(l, nullptr, &end);
+  return end;
+}
 
 cudaError_t launch_lora(const Lora& l, void* ws, cudaStream_t st) {
+  if (l.R >= kTilesFrom) {
+    size_t end = 0;
+    const Plan p = plan_at(l, ws, &end);
+    const size_t smem = (size_t)(l.G + 1) * 4;
+    cudaError_t e = allow_smem(k_plan, smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(k_plan, dim3(1), dim3(1024), smem, st, l, p);
+    if (e != cudaSuccess) return e;
+    switch (rank_pad(l.rank)) {
+      case 16: return run_tiles<16>(l, p, st);
+      case 32: return run_tiles<32>(l, p, st);
+      case 64: return run_tiles<64>(l, p, st);
+      default: return run_tiles<128>(l, p, st);
+    }
+  }
   float* t = static_cast<float*>(ws);
   // ranks per block: more blocks for few rows, fewer passes over x for many
   const int64_t pairs = l.R * l.rank;

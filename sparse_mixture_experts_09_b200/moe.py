@@ -776,28 +776,19 @@ class RouterLosses(NamedTuple):
     prob_mean: torch.Tensor
 
 
-class _On:
-    """The device and stream of a call, current for its length, so that outputs and scratch
-    belong to the stream the kernels run on. device: the call's first tensor's."""
-
-    def __init__(self, device: torch.device, stream):
-        self.device, self.stream = device, stream
-        self.inside = None
-
-    def __enter__(self):
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                raise ValueError(f"the stream is on {self.stream.device}, the tensors on {self.device}")
-            self.inside = torch.cuda.stream(self.stream)
-        elif self.device.index != torch.cuda.current_device():
-            self.inside = torch.cuda.device(self.device)
-        if self.inside is not None:
-            self.inside.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        if self.inside is not None:
-            self.inside.__exit__(*exc)
+def _on(device: torch.device, stream, call):
+    """call(raw stream) with the tensors' device and the stream current, so that the outputs and
+    scratch it allocates belong to the stream that its kernels run on."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            # the raw handle alone: building a Stream object costs 3 us a call
+            return call(torch._C._cuda_getCurrentRawStream(device.index))
+        with torch.cuda.device(device):
+            return call(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
 def _arg(t, name: str, dtypes, shape, device=None) -> Optional[int]:
@@ -844,11 +835,14 @@ def route(logits, routing: Routing, bias=None, stream=None):
     t, e = logits.shape
     dev = logits.device
     b = None if bias is None else _arg(bias, "bias", _F32, (e,), dev)
-    with _On(dev, stream) as st:
+
+    def call(st):
         idx = torch.empty((t, routing.k), dtype=torch.int32, device=dev)
         w = torch.empty((t, routing.k), dtype=torch.float32, device=dev)
         _check(lib().moe_route(args, logits.data_ptr(), b, idx.data_ptr(), w.data_ptr(), st))
-    return idx, w
+        return idx, w
+
+    return _on(dev, stream, call)
 
 
 def _token_mask(mask, t: int, dev) -> Optional[int]:
@@ -864,7 +858,8 @@ def router_losses(logits, topk_idx, routing: Routing, token_mask=None, stream=No
     dev = logits.device
     idx = _arg(topk_idx, "topk_idx", _I32, (t, routing.k), dev)
     mask = _token_mask(token_mask, t, dev)
-    with _On(dev, stream) as st:
+
+    def call(st):
         n = lib().moe_router_losses_workspace(args)
         ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
         losses = torch.empty(2, dtype=torch.float32, device=dev)
@@ -872,7 +867,9 @@ def router_losses(logits, topk_idx, routing: Routing, token_mask=None, stream=No
         prob = torch.empty(e, dtype=torch.float32, device=dev)
         _check(lib().moe_router_losses(args, logits.data_ptr(), idx, mask, losses.data_ptr(),
                                        counts.data_ptr(), prob.data_ptr(), ws.data_ptr(), n, st))
-    return RouterLosses(losses, counts, prob)
+        return RouterLosses(losses, counts, prob)
+
+    return _on(dev, stream, call)
 
 
 def route_backward(logits, topk_idx, routing: Routing, d_topk_w=None, counts=None, d_losses=None,
@@ -889,11 +886,14 @@ def route_backward(logits, topk_idx, routing: Routing, d_topk_w=None, counts=Non
     c = None if counts is None else _arg(counts, "counts", _I32, (e + 1,), dev)
     dl = None if d_losses is None else _arg(d_losses, "d_losses", _F32, (2,), dev)
     mask = _token_mask(token_mask, t, dev)
-    with _On(dev, stream) as st:
+
+    def call(st):
         out = torch.empty((t, e), dtype=logits.dtype, device=dev)
         _check(lib().moe_route_backward(args, logits.data_ptr(), idx, dw, c, dl, mask,
                                         out.data_ptr(), st))
-    return out
+        return out
+
+    return _on(dev, stream, call)
 
 
 def combine_backward(d_out, y_perm, row_of, topk_w, counts=None, offsets=None, need_dy: bool = True,
@@ -918,12 +918,15 @@ def combine_backward(d_out, y_perm, row_of, topk_w, counts=None, offsets=None, n
         e = counts.numel()
         c = _arg(counts, "counts", _I32, (e,), dev)
         o = _arg(offsets, "offsets", _I32, (e + 1,), dev)
-    with _On(dev, stream) as st:
+
+    def call(st):
         dy = torch.empty((rows, h), dtype=torch.float32, device=dev) if need_dy else None
         dw = torch.empty((t, k), dtype=torch.float32, device=dev) if need_dw else None
         _check(lib().moe_combine_backward(d, y, r, w, c, o, dy.data_ptr() if need_dy else None,
                                           dw.data_ptr() if need_dw else None, t, k, h, e, rows, st))
-    return dy, dw
+        return dy, dw
+
+    return _on(dev, stream, call)
 
 
 # ---- low-rank adapters of many requests beside a shared projection ----
@@ -960,12 +963,14 @@ def lora_add(base, x, a, b, adapter, scale=None, out=None, stream=None):
     ip = _arg(adapter, "adapter", _I32, (r,), dev)
     sp = None if scale is None else _arg(scale, "scale", _F32, (ad,), dev)
     base_p, base_s = _rows(base, "base", _LOGITS, (r, n), dev)
-    with _On(dev, stream) as st:
-        if out is None:
-            out = torch.empty((r, n), dtype=base.dtype, device=dev)
-        out_p, out_s = _rows(out, "out", (base.dtype,), (r, n), dev)
+
+    def call(st):
+        dst = torch.empty((r, n), dtype=base.dtype, device=dev) if out is None else out
+        out_p, out_s = _rows(dst, "out", (base.dtype,), (r, n), dev)
         args = _LoraArgs(r, xs, base_s, out_s, h, n, rank, ad, int(base.dtype == torch.float32))
         size = lib().moe_lora_workspace(args)
         ws = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
         _check(lib().moe_lora_add(args, base_p, xp, ap, bp, ip, sp, out_p, ws.data_ptr(), size, st))
-    return out
+        return dst
+
+    return _on(dev, stream, call)
