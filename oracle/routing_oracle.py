@@ -45,11 +45,11 @@ def route(logits, k: int, scoring="softmax", num_groups=1, topk_groups=1, group_
     l = clean(logits)
     t_count, e_count = l.shape
     s = scores(l, scoring)
-    if bias is None and group_top == 1:
-        c = l                       # both scores rise with the logit
-    else:
-        c = s + (0.0 if bias is None else np.asarray(bias, dtype=np.float64))
-        c = np.where(np.isnan(c), -np.inf, c)
+    # without a bias experts are compared by their logits (both scores rise with them), and
+    # so are groups by one expert each
+    c = l if bias is None else s + np.asarray(bias, dtype=np.float64)
+    c = np.where(np.isnan(c), -np.inf, c)
+    by_group = s if bias is None and group_top > 1 else c
     gs = e_count // num_groups
     idx = np.empty((t_count, k), dtype=np.int32)
     for t in range(t_count):
@@ -57,7 +57,7 @@ def route(logits, k: int, scoring="softmax", num_groups=1, topk_groups=1, group_
         if num_groups > 1:
             value = []
             for g in range(num_groups):
-                v = np.sort(c[t, g * gs:(g + 1) * gs])[::-1]
+                v = np.sort(by_group[t, g * gs:(g + 1) * gs])[::-1]
                 value.append(v[:group_top].sum())
             free = np.ones(num_groups, dtype=bool)
             for _ in range(topk_groups):

@@ -2,8 +2,9 @@
 // in the logits. Formulas and conventions: include/moe.h.
 //
 // All three kernels give a token L lanes of a warp (L = 8, 16 or 32) and each lane V
-// neighbouring experts, L * V >= E, so that small expert counts fill the warp with
-// several tokens and large ones keep a token's logits in registers.
+// neighbouring experts, L * V >= E: a token's logits stay in registers, and L is the
+// least that holds a slot per lane with V at most 8 (16 above 256 experts), so that one
+// instruction serves several tokens.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -49,6 +50,18 @@ struct Team {
     for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
     return v;
   }
+  __device__ uint32_t max(uint32_t v) const {
+    if constexpr (L == 32) {
+      return __reduce_max_sync(0xffffffffu, v);
+    } else {
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) {
+        const uint32_t w = __shfl_xor_sync(mask, v, o);
+        v = w > v ? w : v;
+      }
+      return v;
+    }
+  }
   // the largest key; among equal keys the lowest index
   __device__ void best(double& key, int& at) const {
 #pragma unroll
@@ -67,120 +80,312 @@ struct Team {
   }
 };
 
+// This lane's logits, cleaned; experts past E count as -inf. vec: rows start on a boundary
+// of the lane's V logits (16 bytes at most) and E is a multiple of V.
+template <typename T, int V>
+__device__ __forceinline__ void load_logits(const T* row, int rank, int E, bool vec, float (&l)[V]) {
+  constexpr int kBytes = V * (int)sizeof(T);
+  const int e0 = rank * V;
+  if (vec && kBytes >= 4) {
+    uint32_t q[(kBytes + 3) / 4];
+    if (e0 < E) {
+      const char* p = reinterpret_cast<const char*>(row + e0);
+      if constexpr (kBytes >= 16) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          q[4 * i] = v.x, q[4 * i + 1] = v.y, q[4 * i + 2] = v.z, q[4 * i + 3] = v.w;
+        }
+      } else if constexpr (kBytes == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        q[0] = v.x, q[1] = v.y;
+      } else {
+        q[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float f;
+      if constexpr (sizeof(T) == 4)
+        f = __uint_as_float(q[v]);
+      else
+        f = __uint_as_float(v & 1 ? q[v / 2] & 0xFFFF0000u : q[v / 2] << 16);
+      l[v] = e0 < E ? clean(f) : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = e0 + v < E ? clean(logit_at(row + e0 + v)) : -INFINITY;
+  }
+}
+
 constexpr int kNone = 0x7fffffff;
 
-// Selection keys are doubles: distinct float logits then have distinct scores but where
-// a score saturates, so the choice does not hang on a rounding of the scores. With no bias
-// and one group the logits themselves are the keys (both scores rise with the logit).
+// Floats as unsigned numbers of the same order (-0 as +0); every float is above 0.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f + 0.f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ ((uint32_t)((int32_t)~u >> 31) | 0x80000000u));
+}
+
+// The choice in double, for tokens whose fp32 values are too close to call and for group
+// values of more than two experts: one arg-max over the lanes at a time. Returns the expert
+// of slot `rank`. Apart from the kernel so that its registers are not the fast path's.
+template <typename T, int L, int V>
+__device__ __noinline__ int choose_in_double(const Routing r, const T* row, const float* bias) {
+  const Team<L> team;
+  const int gs = r.E / r.groups;
+  float l[V];
+  double key[V];
+  load_logits<T, V>(row, team.rank, r.E, false, l);
+  float mx = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
+  mx = team.max(mx);
+  double total = 1.0;
+  if (!r.sigmoid) {
+    total = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (l[v] > -INFINITY) total += exp((double)l[v] - (double)mx);
+    total = team.sum(total);
+    if (total == 0.0) total = 1.0;  // no expert has a score
+  }
+  unsigned open = 0;  // experts of this lane that may still be chosen
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = team.rank * V + v;
+    if (e >= r.E) continue;
+    open |= 1u << v;
+    key[v] = l[v] == -INFINITY ? 0.0
+             : r.sigmoid       ? 1.0 / (1.0 + exp(-(double)l[v]))
+                               : exp((double)l[v] - (double)mx) / total;
+    if (bias) key[v] += (double)__ldg(bias + e);
+    if (!(key[v] == key[v])) key[v] = -INFINITY;
+  }
+  if (r.groups > 1) {
+    constexpr int kSlots = (32 + L - 1) / L;
+    double value[kSlots];  // group g's value in lane g % L, slot g / L
+#pragma unroll
+    for (int q = 0; q < kSlots; ++q) value[q] = -INFINITY;
+    for (int g = 0; g < r.groups; ++g) {
+      unsigned left = open;
+      double sum = 0.0;
+      for (int m = 0; m < r.group_top; ++m) {
+        double k1 = -INFINITY;
+        int at = kNone;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int e = team.rank * V + v;
+          if ((left >> v & 1u) && e / gs == g && (at == kNone || key[v] > k1)) {
+            k1 = key[v];
+            at = e;
+          }
+        }
+        team.best(k1, at);
+        sum += k1;
+        if (at / V == team.rank) left &= ~(1u << (at % V));
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q)
+        if (g == q * L + team.rank) value[q] = sum;
+    }
+    unsigned stay = 0;  // groups, the same in every lane
+    for (int m = 0; m < r.topk_groups; ++m) {
+      double k1 = -INFINITY;
+      int at = kNone;
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        const int g = q * L + team.rank;
+        if (g < r.groups && !(stay >> g & 1u) && (at == kNone || value[q] > k1)) {
+          k1 = value[q];
+          at = g;
+        }
+      }
+      team.best(k1, at);
+      stay |= 1u << at;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if ((open >> v & 1u) && !(stay >> ((team.rank * V + v) / gs) & 1u)) open &= ~(1u << v);
+  }
+  if (!bias) {  // the logits order the experts
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = l[v];
+  }
+  int mine = -1;
+  for (int j = 0; j < r.k; ++j) {
+    double k1 = -INFINITY;
+    int at = kNone;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if ((open >> v & 1u) && (at == kNone || key[v] > k1)) {
+        k1 = key[v];
+        at = team.rank * V + v;
+      }
+    team.best(k1, at);
+    if (at / V == team.rank) open &= ~(1u << (at % V));
+    if (j == team.rank) mine = at;
+  }
+  return mine;
+}
+
+// Routing, one team of L lanes per token. The logits alone decide where nothing else is
+// asked for (both scores rise with the logit, so fp32 is exact); else the values s + bias
+// and the groups' sums are formed in fp32, and a token two of whose compared values lie
+// within the sums of their error bounds is chosen again in double (about one token in
+// a thousand): fp32 work, decisions as in double. Bounds, u = 2^-24: a sigmoid is off by
+// 4u (exponential, two ulp) + 2u, a softmax by at most 32u of the largest probability
+// (exponential 4u, its argument's rounding, a sum of up to 512 terms in a tree, a
+// division), and the sum with the bias by u of its value.
+//
+// The k largest are taken one by one: each lane keeps the largest of its own values, the
+// team finds the largest of those, the lowest lane that has it gives its lowest expert.
+// Bound by instructions, not bytes: a team is as narrow as 8 values per lane allow, so
+// that a warp's instruction serves up to four tokens.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(32 * kWarps) k_route(const Routing r, const T* __restrict__ logits,
-                                                       const float* __restrict__ bias,
+                                                       const float* __restrict__ bias, int vec,
                                                        int32_t* __restrict__ idx_out,
                                                        float* __restrict__ w_out) {
   pdl_trigger();
   pdl_wait();
+  __shared__ float s_value[kWarps * 32 / L][L * V + 1];
   const Team<L> team;
   constexpr int kPer = 32 / L * kWarps;  // tokens per block
+  float* value_of = s_value[threadIdx.x / L];
   const int gs = r.E / r.groups;
+  const bool grouped = r.groups > 1;
+  const bool scores = bias || r.group_top > 1;
+  // lanes of a group: a power of two, so that they can reduce among themselves
+  int lanes = L;
+  while (lanes * r.groups > L) lanes >>= 1;
+  const bool narrow = lanes > 0 && r.group_top <= 2;
+  int bit[V];  // of each of the lane's experts' groups in `stay`
+#pragma unroll
+  for (int v = 0; v < V; ++v) bit[v] = grouped ? team.base + (team.rank * V + v) / gs * lanes : 0;
   for (int64_t t0 = (int64_t)blockIdx.x * kPer; t0 < r.T; t0 += (int64_t)gridDim.x * kPer) {
     const int64_t t = t0 + threadIdx.x / L;
     if (t >= r.T) continue;  // a token's lanes leave together
     const T* row = logits + t * r.stride;
-    float l[V];
-    double key[V];
-    float mx = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = team.rank * V + v;
-      l[v] = e < r.E ? clean(logit_at(row + e)) : -INFINITY;
-      mx = fmaxf(mx, l[v]);
-    }
-    mx = team.max(mx);
-    const bool scores = bias || r.group_top > 1;
-    double total = 1.0;
+    float l[V], c[V];
+    load_logits<T, V>(row, team.rank, r.E, vec, l);
+    float mx = -INFINITY, tol = 0.f, sum = 1.f;
     if (!r.sigmoid && (scores || !r.renorm)) {
-      total = 0.0;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (l[v] > -INFINITY) total += exp((double)l[v] - (double)mx);
-      total = team.sum(total);
-      if (total == 0.0) total = 1.0;  // no expert has a score
+      for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
+      mx = team.max(mx);
     }
-    unsigned open = 0;  // experts of this lane that may still be chosen
+    if (scores) {
+      if (r.sigmoid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = team.rank * V + v;
-      if (e >= r.E) continue;
-      open |= 1u << v;
-      key[v] = l[v];
-      if (scores) {
-        key[v] = l[v] == -INFINITY ? 0.0
-                 : r.sigmoid       ? 1.0 / (1.0 + exp(-(double)l[v]))
-                                   : exp((double)l[v] - (double)mx) / total;
-        if (bias) key[v] += (double)__ldg(bias + e);
-        if (!(key[v] == key[v])) key[v] = -INFINITY;
+        for (int v = 0; v < V; ++v) c[v] = l[v] > -INFINITY ? 1.f / (1.f + expf(-l[v])) : 0.f;
+        tol = 0x1p-20f;
+      } else {
+        sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          c[v] = l[v] > -INFINITY ? expf(l[v] - mx) : 0.f;
+          sum += c[v];
+        }
+        sum = team.sum(sum);
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) c[v] *= inv;
+        tol = 0x1p-18f * inv;  // the largest probability is 1 / sum
+      }
+      if (bias) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int e = team.rank * V + v;
+          if (e < r.E) c[v] += __ldg(bias + e);
+          if (!(c[v] == c[v])) c[v] = -INFINITY;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) c[v] = l[v];
+    }
+    bool close = false;
+    unsigned stay = 0xffffffffu;  // bit base + g * lanes: group g stays
+    if (grouped) {
+      close = !narrow;
+      if (narrow) {
+        __syncwarp(team.mask);
+#pragma unroll
+        for (int v = 0; v < V; ++v) value_of[team.rank * V + v] = c[v];
+        __syncwarp(team.mask);
+        const int g = team.rank / lanes;
+        float m1 = -INFINITY, m2 = -INFINITY;
+        if (g < r.groups) {
+          for (int i = team.rank - g * lanes; i < gs; i += lanes) {
+            const float v = value_of[g * gs + i];
+            m2 = fmaxf(m2, fminf(v, m1));
+            m1 = fmaxf(m1, v);
+          }
+        }
+        for (int o = lanes >> 1; o > 0; o >>= 1) {
+          const float o1 = __shfl_xor_sync(team.mask, m1, o), o2 = __shfl_xor_sync(team.mask, m2, o);
+          m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+          m1 = fmaxf(m1, o1);
+        }
+        const float value = r.group_top == 2 ? m1 + m2 : m1;
+        // what the group's value may be off by: its terms' bounds and their sum's rounding
+        const float off = 2.f * tol + 0x1p-21f * (fabsf(m1) + (r.group_top == 2 ? fabsf(m2) : 0.f));
+        int above = 0;
+        for (int j = 0; j < r.groups; ++j) {
+          const float other = team.from(value, j * lanes);
+          above += other > value || (other == value && j < g);
+          if (scores) {
+            const float reach = off + team.from(off, j * lanes);
+            if (j != g && g < r.groups && !(fabsf(other - value) > reach)) close = true;
+          }
+        }
+        stay = __ballot_sync(team.mask, above < r.topk_groups);
+        close = __any_sync(team.mask, close);
       }
     }
-    if (r.groups > 1) {
-      double value[32 / L > 0 ? (32 + L - 1) / L : 1];  // group g's value in lane g % L, slot g / L
-      constexpr int kSlots = (32 + L - 1) / L;
+    int mine = -1;
+    if (!close) {
+      uint32_t key[V], top = 0;
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) value[q] = -INFINITY;
-      for (int g = 0; g < r.groups; ++g) {
-        unsigned left = open;
-        double sum = 0.0;
-        for (int m = 0; m < r.group_top; ++m) {
-          double k1 = -INFINITY;
-          int at = kNone;
+      for (int v = 0; v < V; ++v) {
+        const int e = team.rank * V + v;
+        const bool open = e < r.E && (!grouped || (stay >> bit[v] & 1u));
+        key[v] = open ? ordered(bias ? c[v] : l[v]) : 0u;
+        top = key[v] > top ? key[v] : top;
+      }
+      float before = 0.f;
+      const int passes = bias ? r.k + 1 : r.k;  // one more to see how far the next one is
+      for (int j = 0; j < passes; ++j) {
+        const uint32_t m = team.max(top);
+        if (bias) {
+          const float now = unordered(m);
+          if (j > 0 && m != 0 && !(before - now > 2.f * tol + 0x1p-21f * fabsf(before))) close = true;
+          before = now;
+          if (j == r.k) break;
+        }
+        const int src = __ffs(__ballot_sync(team.mask, top == m)) - 1;
+        int e = 0;
+        if ((int)(threadIdx.x & 31) == src) {
+          int at = 0;
+#pragma unroll
+          for (int v = V - 1; v >= 0; --v)
+            if (key[v] == m) at = v;
+          top = 0;
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            const int e = team.rank * V + v;
-            if ((left >> v & 1u) && e / gs == g && (at == kNone || key[v] > k1)) {
-              k1 = key[v];
-              at = e;
-            }
+            if (v == at) key[v] = 0;
+            top = key[v] > top ? key[v] : top;
           }
-          team.best(k1, at);
-          sum += k1;
-          if (at / V == team.rank) left &= ~(1u << (at % V));
+          e = team.rank * V + at;
         }
-#pragma unroll
-        for (int q = 0; q < kSlots; ++q)
-          if (g == q * L + team.rank) value[q] = sum;
+        e = __shfl_sync(team.mask, e, src);
+        if (j == team.rank) mine = e;
       }
-      unsigned stay = 0;  // groups, the same in every lane
-      for (int m = 0; m < r.topk_groups; ++m) {
-        double k1 = -INFINITY;
-        int at = kNone;
-#pragma unroll
-        for (int q = 0; q < kSlots; ++q) {
-          const int g = q * L + team.rank;
-          if (g < r.groups && !(stay >> g & 1u) && (at == kNone || value[q] > k1)) {
-            k1 = value[q];
-            at = g;
-          }
-        }
-        team.best(k1, at);
-        stay |= 1u << at;
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if ((open >> v & 1u) && !(stay >> ((team.rank * V + v) / gs) & 1u)) open &= ~(1u << v);
     }
-    int mine = -1;  // the expert of slot `rank`
-    for (int j = 0; j < r.k; ++j) {
-      double k1 = -INFINITY;
-      int at = kNone;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if ((open >> v & 1u) && (at == kNone || key[v] > k1)) {
-          k1 = key[v];
-          at = team.rank * V + v;
-        }
-      team.best(k1, at);
-      if (at / V == team.rank) open &= ~(1u << (at % V));
-      if (j == team.rank) mine = at;
-    }
+    if (close) mine = choose_in_double<T, L, V>(r, row, bias);
     // weights: one lane per slot, in double, rounded once
     const bool slot = team.rank < r.k;
     const float ls = slot ? clean(logit_at(row + mine)) : -INFINITY;
@@ -188,10 +393,15 @@ __global__ void __launch_bounds__(32 * kWarps) k_route(const Routing r, const T*
     if (r.sigmoid) {
       if (ls > -INFINITY) s = 1.0 / (1.0 + exp(-(double)ls));
     } else if (r.renorm) {  // the sum over all experts cancels
-      const float top = team.max(ls);
-      if (ls > -INFINITY) s = exp((double)ls - (double)top);
-    } else if (ls > -INFINITY) {
-      s = exp((double)ls - (double)mx) / total;
+      const float most = team.max(ls);
+      if (ls > -INFINITY) s = exp((double)ls - (double)most);
+    } else {
+      double total = 0.0;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (l[v] > -INFINITY) total += exp((double)l[v] - (double)mx);
+      total = team.sum(total);
+      if (ls > -INFINITY) s = exp((double)ls - (double)mx) / total;
     }
     if (r.renorm) {
       const double all = team.sum(s);
@@ -210,7 +420,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_route(const Routing r, const T*
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(32 * kWarps) k_losses(const Routing r, const T* __restrict__ logits,
                                                         const int32_t* __restrict__ idx,
-                                                        const uint8_t* __restrict__ mask,
+                                                        const uint8_t* __restrict__ mask, int vec,
                                                         double* __restrict__ part_sum,
                                                         int32_t* __restrict__ part_count) {
   pdl_trigger();
@@ -231,12 +441,9 @@ __global__ void __launch_bounds__(32 * kWarps) k_losses(const Routing r, const T
     if (t >= r.T || (mask && !mask[t])) continue;
     const T* row = logits + t * r.stride;
     float l[V], mx = -INFINITY;
+    load_logits<T, V>(row, team.rank, r.E, vec, l);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = team.rank * V + v;
-      l[v] = e < r.E ? clean(logit_at(row + e)) : -INFINITY;
-      mx = fmaxf(mx, l[v]);
-    }
+    for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
     mx = team.max(mx);
     float x[V], sum = 0.f;
 #pragma unroll
@@ -353,7 +560,7 @@ template <typename T, int L, int V>
 __global__ void __launch_bounds__(32 * kWarps)
     k_route_bwd(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
                 const float* __restrict__ d_w, const int32_t* __restrict__ counts,
-                const float* __restrict__ d_losses, const uint8_t* __restrict__ mask,
+                const float* __restrict__ d_losses, const uint8_t* __restrict__ mask, int vec,
                 T* __restrict__ d_logits) {
   pdl_trigger();
   pdl_wait();
@@ -378,12 +585,9 @@ __global__ void __launch_bounds__(32 * kWarps)
     const T* row = logits + t * r.stride;
     const bool losses = d_losses && (!mask || mask[t]);
     float l[V], mx = -INFINITY;
+    load_logits<T, V>(row, team.rank, r.E, vec, l);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = team.rank * V + v;
-      l[v] = e < r.E ? clean(logit_at(row + e)) : -INFINITY;
-      mx = fmaxf(mx, l[v]);
-    }
+    for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
     // the chosen experts, one per lane: what arrives at their scores
     int my_e = -1;
     float g = 0.f, ls = -INFINITY;
@@ -489,35 +693,56 @@ unsigned token_blocks(const Routing& r, int waves) {
   return (unsigned)(want < cap ? want : cap);
 }
 
+template <int L, int V, typename F>
+cudaError_t with(F f) {
+  return f(std::integral_constant<int, L>(), std::integral_constant<int, V>());
+}
+
 template <typename F>
-cudaError_t by_experts(int E, F f) {
-  if (E <= 8) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
-  if (E <= 16) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 1>());
-  if (E <= 32) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
-  if (E <= 64) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 2>());
-  if (E <= 128) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 4>());
-  if (E <= 256) return f(std::integral_constant<int, 32>(), std::integral_constant<int, 8>());
-  return f(std::integral_constant<int, 32>(), std::integral_constant<int, 16>());
+cudaError_t by_sizes(const Routing& r, F f) {
+  if (r.k <= 8 && r.groups <= 8) {  // a lane per slot, and one per group at least
+    if (r.E <= 8) return with<8, 1>(f);
+    if (r.E <= 16) return with<8, 2>(f);
+    if (r.E <= 32) return with<8, 4>(f);
+    if (r.E <= 64) return with<8, 8>(f);
+    if (r.E <= 128) return with<16, 8>(f);
+  } else {
+    if (r.E <= 64) return with<32, 2>(f);
+    if (r.E <= 128) return with<32, 4>(f);
+  }
+  if (r.E <= 256) return with<32, 8>(f);
+  return with<32, 16>(f);
+}
+
+// Whether every lane's V logits start on a boundary of their size (16 bytes at most).
+template <typename T, int V>
+int vectors(const Routing& r, const T* logits) {
+  constexpr size_t kBytes = V * sizeof(T) < 16 ? V * sizeof(T) : 16;
+  return r.E % V == 0 && reinterpret_cast<uintptr_t>(logits) % kBytes == 0 &&
+         (r.T == 1 || r.stride * (int64_t)sizeof(T) % (int64_t)kBytes == 0);
 }
 
 }  // namespace
 
 cudaError_t launch_route(const Routing& r, const void* logits, const float* bias, int32_t* idx,
                          float* w, cudaStream_t st) {
-  return by_experts(r.E, [&](auto l, auto v) {
+  return by_sizes(r, [&](auto l, auto v) {
     constexpr int L = decltype(l)::value, V = decltype(v)::value;
     const dim3 grid(token_blocks<L>(r, 8)), block(32 * kWarps);
-    if (r.bf16)
-      return launch_pdl(k_route<__nv_bfloat16, L, V>, grid, block, 0, st, r,
-                        static_cast<const __nv_bfloat16*>(logits), bias, idx, w);
-    return launch_pdl(k_route<float, L, V>, grid, block, 0, st, r,
-                      static_cast<const float*>(logits), bias, idx, w);
+    if (r.bf16) {
+      const auto* p = static_cast<const __nv_bfloat16*>(logits);
+      return launch_pdl(k_route<__nv_bfloat16, L, V>, grid, block, 0, st, r, p, bias,
+                        vectors<__nv_bfloat16, V>(r, p), idx, w);
+    }
+    const auto* p = static_cast<const float*>(logits);
+    return launch_pdl(k_route<float, L, V>, grid, block, 0, st, r, p, bias,
+                      vectors<float, V>(r, p), idx, w);
   });
 }
 
 int router_loss_blocks(const Routing& r) {
   int n = 0;
-  by_experts(r.E, [&](auto l, auto) {
+  by_sizes(r, [&](auto l, auto) {
     n = (int)token_blocks<decltype(l)::value>(r, 2);
     return cudaSuccess;
   });
@@ -530,14 +755,17 @@ cudaError_t launch_router_losses(const Routing& r, const void* logits, const int
                                  cudaStream_t st) {
   const int blocks = router_loss_blocks(r);
   if (blocks > 0) {
-    const cudaError_t e = by_experts(r.E, [&](auto l, auto v) {
+    const cudaError_t e = by_sizes(r, [&](auto l, auto v) {
       constexpr int L = decltype(l)::value, V = decltype(v)::value;
       const dim3 grid((unsigned)blocks), block(32 * kWarps);
-      if (r.bf16)
-        return launch_pdl(k_losses<__nv_bfloat16, L, V>, grid, block, 0, st, r,
-                          static_cast<const __nv_bfloat16*>(logits), idx, mask, part_sum, part_count);
-      return launch_pdl(k_losses<float, L, V>, grid, block, 0, st, r,
-                        static_cast<const float*>(logits), idx, mask, part_sum, part_count);
+      if (r.bf16) {
+        const auto* p = static_cast<const __nv_bfloat16*>(logits);
+        return launch_pdl(k_losses<__nv_bfloat16, L, V>, grid, block, 0, st, r, p, idx, mask,
+                          vectors<__nv_bfloat16, V>(r, p), part_sum, part_count);
+      }
+      const auto* p = static_cast<const float*>(logits);
+      return launch_pdl(k_losses<float, L, V>, grid, block, 0, st, r, p, idx, mask,
+                        vectors<float, V>(r, p), part_sum, part_count);
     });
     if (e != cudaSuccess) return e;
   }
@@ -548,16 +776,18 @@ cudaError_t launch_router_losses(const Routing& r, const void* logits, const int
 cudaError_t launch_route_backward(const Routing& r, const void* logits, const int32_t* idx,
                                   const float* d_w, const int32_t* counts, const float* d_losses,
                                   const uint8_t* mask, void* d_logits, cudaStream_t st) {
-  return by_experts(r.E, [&](auto l, auto v) {
+  return by_sizes(r, [&](auto l, auto v) {
     constexpr int L = decltype(l)::value, V = decltype(v)::value;
     const dim3 grid(token_blocks<L>(r, 8)), block(32 * kWarps);
-    if (r.bf16)
-      return launch_pdl(k_route_bwd<__nv_bfloat16, L, V>, grid, block, 0, st, r,
-                        static_cast<const __nv_bfloat16*>(logits), idx, d_w, counts, d_losses, mask,
+    if (r.bf16) {
+      const auto* p = static_cast<const __nv_bfloat16*>(logits);
+      return launch_pdl(k_route_bwd<__nv_bfloat16, L, V>, grid, block, 0, st, r, p, idx, d_w, counts,
+                        d_losses, mask, vectors<__nv_bfloat16, V>(r, p),
                         static_cast<__nv_bfloat16*>(d_logits));
-    return launch_pdl(k_route_bwd<float, L, V>, grid, block, 0, st, r,
-                      static_cast<const float*>(logits), idx, d_w, counts, d_losses, mask,
-                      static_cast<float*>(d_logits));
+    }
+    const auto* p = static_cast<const float*>(logits);
+    return launch_pdl(k_route_bwd<float, L, V>, grid, block, 0, st, r, p, idx, d_w, counts, d_losses,
+                      mask, vectors<float, V>(r, p), static_cast<float*>(d_logits));
   });
 }
 

@@ -101,6 +101,38 @@ def test_route_large_values_and_wide_ranges():
             _check_route(l, M.Routing(3, scoring, renormalize=renorm))
 
 
+def test_route_signed_zeros_are_equal():
+    l = torch.tensor([[-0.0, 0.0, -1.0, -0.0], [0.0, -0.0, 0.0, -2.0]])
+    idx, _ = _check_route(l, M.Routing(3))
+    assert idx.tolist() == [[0, 1, 3], [0, 1, 2]]
+
+
+@pytest.mark.parametrize("e,k,groups,top,m", [(8, 3, 1, 1, 1), (64, 8, 8, 4, 1), (256, 8, 8, 4, 1), (64, 6, 16, 4, 1),
+                                              (120, 8, 8, 3, 1), (512, 32, 32, 8, 1), (48, 12, 4, 2, 1)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_near_ties_are_decided_exactly(e, k, groups, top, m, scoring):
+    """Scores a few fp32 steps apart around the same few values: fp32 sums cannot tell them
+    apart, double ones can (differences above 2^-34 against errors of 2^-50). Sums of a
+    group's two best are left out: those can tie to within double's error."""
+    g = torch.Generator().manual_seed(e + k)
+    t = 300
+    l = torch.randint(-1, 2, (t, e), generator=g).float() * 0.5
+    step = torch.stack([torch.randperm(e, generator=g) for _ in range(t)]).float()
+    l = l + step * 2.0 ** -23 * 0.5
+    _check_route(l, M.Routing(k, scoring, groups, top, m))
+    bias = (torch.randint(-1, 2, (e,), generator=g).float() * 0.25)
+    _check_route(l, M.Routing(k, scoring, groups, top, m), bias)
+
+
+def test_route_huge_biases():
+    l = _logits(64, 64, 3, "normal")
+    g = torch.Generator().manual_seed(8)
+    for size in (1e3, 1e30, 3e38):
+        bias = torch.randint(-1, 2, (64,), generator=g).float() * size
+        _check_route(l, M.Routing(5, "sigmoid", 8, 3, 2), bias)
+        _check_route(l, M.Routing(5, "softmax"), bias)
+
+
 def test_route_matches_the_layers_router():
     """The default rule on the layer's own logits is the layer's own routing."""
     g = torch.Generator().manual_seed(2)
