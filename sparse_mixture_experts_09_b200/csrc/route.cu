@@ -2,9 +2,8 @@
 // in the logits. Formulas and conventions: include/moe.h.
 //
 // All three kernels give a token L lanes of a warp (L = 8, 16 or 32) and each lane V
-// neighbouring experts, L * V >= E: a token's logits stay in registers, and L is the
-// least that holds a slot per lane with V at most 8 (16 above 256 experts), so that one
-// instruction serves several tokens.
+// neighbouring experts, L * V >= E: a token's logits stay in registers, and L is small,
+// so that one instruction serves several tokens, but holds a lane per slot.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -24,8 +23,15 @@ __device__ __forceinline__ float logit_at(const __nv_bfloat16* p) {
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// sigmoid(l) and 1 - sigmoid(l), each to within a few units of its own last place.
+__device__ __forceinline__ void sigmoid_pair(float l, float& s, float& rest) {
+  const float x = expf(-fabsf(l)), big = __fdividef(1.f, 1.f + x), small = x * big;
+  s = l >= 0.f ? big : small;
+  rest = l >= 0.f ? small : big;
+}
+
 // NaN -> -inf, +inf -> the largest float: exp(l - max) is then 0 or finite everywhere.
-__device__ __forceinline__ float clean(float l) { return l == l ? fminf(l, FLT_MAX) : -INFINITY; }
+__device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
 // The lanes of one token, and butterfly reductions over them.
 template <int L>
@@ -50,6 +56,11 @@ struct Team {
     for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
     return v;
   }
+  __device__ double max(double v) const {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(mask, v, o));
+    return v;
+  }
   __device__ uint32_t max(uint32_t v) const {
     if constexpr (L == 32) {
       return __reduce_max_sync(0xffffffffu, v);
@@ -62,17 +73,13 @@ struct Team {
       return v;
     }
   }
-  // the largest key; among equal keys the lowest index
-  __device__ void best(double& key, int& at) const {
+  __device__ unsigned long long max(unsigned long long v) const {
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) {
-      const double k2 = __shfl_xor_sync(mask, key, o);
-      const int a2 = __shfl_xor_sync(mask, at, o);
-      if (k2 > key || (k2 == key && a2 < at)) {
-        key = k2;
-        at = a2;
-      }
+      const unsigned long long w = __shfl_xor_sync(mask, v, o);
+      v = w > v ? w : v;
     }
+    return v;
   }
   template <typename T>
   __device__ T from(T v, int r) const {
@@ -118,274 +125,418 @@ __device__ __forceinline__ void load_logits(const T* row, int rank, int E, bool 
   }
 }
 
-constexpr int kNone = 0x7fffffff;
+// The reverse of load_logits, one rounding for bf16.
+template <typename T, int V>
+__device__ __forceinline__ void store_row(T* row, int rank, int E, bool vec, const float (&f)[V]) {
+  constexpr int kBytes = V * (int)sizeof(T);
+  const int e0 = rank * V;
+  if (vec && kBytes >= 4) {
+    if (e0 >= E) return;
+    uint32_t q[(kBytes + 3) / 4];
+#pragma unroll
+    for (int i = 0; i < (kBytes + 3) / 4; ++i) {
+      if constexpr (sizeof(T) == 4)
+        q[i] = __float_as_uint(f[i]);
+      else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(q[i]) : "f"(f[(2 * i + 1) % V]), "f"(f[2 * i % V]));
+    }
+    char* p = reinterpret_cast<char*>(row + e0);
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i)
+        reinterpret_cast<uint4*>(p)[i] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+    } else if constexpr (kBytes == 8) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(q[0], q[1]);
+    } else {
+      *reinterpret_cast<uint32_t*>(p) = q[0];
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (e0 + v < E) store(row + e0 + v, f[v]);
+  }
+}
 
-// Floats as unsigned numbers of the same order (-0 as +0); every float is above 0.
+// Floats and doubles as unsigned numbers of the same order (-0 as +0); all are above 0.
 __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t u = __float_as_uint(f + 0.f);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ unsigned long long ordered(double f) {
+  const unsigned long long u = (unsigned long long)__double_as_longlong(f + 0.0);
+  return u ^ ((unsigned long long)((long long)u >> 63) | 0x8000000000000000ull);
 }
 __device__ __forceinline__ float unordered(uint32_t u) {
   return __uint_as_float(u ^ ((uint32_t)((int32_t)~u >> 31) | 0x80000000u));
 }
 
-// The choice in double, for tokens whose fp32 values are too close to call and for group
-// values of more than two experts: one arg-max over the lanes at a time. Returns the expert
-// of slot `rank`. Apart from the kernel so that its registers are not the fast path's.
+template <typename U>
+__device__ __forceinline__ void in_order(U& a, U& b) {  // the larger first
+  const U hi = a > b ? a : b;
+  b = a > b ? b : a;
+  a = hi;
+}
+
+// Descending, by Batcher's odd-even merge (all indices are known at compile time).
+template <typename U, int V>
+__device__ __forceinline__ void sort_down(U (&a)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i >= k % p && (i - k % p) % (2 * k) < k && i + k < V && i / (2 * p) == (i + k) / (2 * p))
+          in_order(a[i], a[i + k]);
+}
+
+// How a team's lanes share the groups: `lanes` of them (a power of two) to a group.
+template <int L, int V>
+struct Groups {
+  int lanes, size;
+  unsigned bits[(V + 3) / 4];  // the lane's experts' groups in a ballot of the warp, a byte each
+  __device__ Groups(const Routing& r, const Team<L>& team) {
+    size = r.E / r.groups;
+    lanes = L;
+    while (lanes * r.groups > L) lanes >>= 1;
+    int g = 0, in = 0;
+    if (r.groups > 1) {
+      g = team.rank * V / size;
+      in = team.rank * V - g * size;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const unsigned b = r.groups > 1 ? team.base + g * lanes : 0;
+      bits[v / 4] = (v % 4 ? bits[v / 4] : 0u) | (b & 31u) << (8 * (v % 4));
+      if (++in == size) {
+        in = 0;
+        ++g;
+      }
+    }
+  }
+  __device__ bool stays(unsigned stay, int v) const {
+    return stay >> (bits[v / 4] >> (8 * (v % 4)) & 31u) & 1u;
+  }
+};
+
+// The groups that stay, as a ballot (bit base + g * lanes for group g). With CHECK a value may
+// be off by tol + 8 u |value|; `close` is set where the last group that stays and the first
+// that goes are not further apart than that allows.
+// A group's one or two best: its lanes take their own values, or every lanes-th from shared
+// memory, and merge their pairs; group_top > 2 takes the largest left group_top times.
+template <bool CHECK, typename K, int L, int V>
+__device__ __forceinline__ unsigned open_groups(const Routing& r, const Team<L>& team,
+                                                const Groups<L, V>& groups, const K (&value)[V], K tol,
+                                                K* shared, bool& close) {
+  const int lanes = groups.lanes, g = team.rank / lanes;
+  const K none = -INFINITY;
+  const auto at_expert = [](int e) { return e + (e >> 5); };  // groups of 32 on distinct banks
+  const bool own = CHECK && groups.size == V * lanes;  // the lanes hold their group's values
+  if (!own) {
+    __syncwarp(team.mask);
+#pragma unroll
+    for (int v = 0; v < V; ++v) shared[at_expert(team.rank * V + v)] = value[v];
+    __syncwarp(team.mask);
+  }
+  K m1 = none, m2 = none;
+  if (CHECK || r.group_top <= 2) {
+    const auto add = [&](K x) {
+      const K low = x < m1 ? x : m1;
+      m2 = low > m2 ? low : m2;
+      m1 = x > m1 ? x : m1;
+    };
+    if (own) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) add(value[v]);
+    } else if (g < r.groups) {
+      for (int i = team.rank - g * lanes; i < groups.size; i += lanes)
+        add(shared[at_expert(g * groups.size + i)]);
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      const K o1 = __shfl_xor_sync(team.mask, m1, o), o2 = __shfl_xor_sync(team.mask, m2, o);
+      const K low = o1 < m1 ? o1 : m1;
+      m2 = o2 > m2 ? o2 : m2;
+      m2 = low > m2 ? low : m2;
+      m1 = o1 > m1 ? o1 : m1;
+    }
+  } else {
+    m1 = 0;
+    for (int n = 0; n < r.group_top; ++n) {
+      K best = none;
+      int at = 0x7fffffff;
+      if (g < r.groups)
+        for (int i = team.rank - g * lanes; i < groups.size; i += lanes) {
+          const K x = shared[at_expert(g * groups.size + i)];
+          if (x > best || (x == best && i < at && x > none)) {
+            best = x;
+            at = i;
+          }
+        }
+      for (int o = lanes >> 1; o > 0; o >>= 1) {
+        const K ob = __shfl_xor_sync(team.mask, best, o);
+        const int oa = __shfl_xor_sync(team.mask, at, o);
+        if (ob > best || (ob == best && oa < at)) {
+          best = ob;
+          at = oa;
+        }
+      }
+      m1 += best;
+      if (at != 0x7fffffff && at % lanes == team.rank - g * lanes) shared[at_expert(g * groups.size + at)] = none;
+    }
+  }
+  const K mine = r.group_top == 2 ? m1 + m2 : m1;
+  int above = 0;
+  for (int j = 0; j < r.groups; ++j) {
+    const K other = team.from(mine, j * lanes);
+    above += other > mine || (other == mine && j < g);
+  }
+  const bool in = above < r.topk_groups;
+  if (CHECK) {
+    const bool real = g < r.groups;
+    const K off = real ? 2 * tol + (K)0x1p-20 * (fabs(m1) + (r.group_top == 2 ? fabs(m2) : (K)0)) : (K)0;
+    const K least = -team.max(real && in ? -mine : none), most = team.max(real && !in ? mine : none);
+    close = r.topk_groups < r.groups && !(least - most > 2 * team.max(off));
+  }
+  return __ballot_sync(team.mask, in);
+}
+
+// The best experts in order, one to a lane: order[v] compares them. Returns the expert of lane
+// `rank` below n. Each lane sorts its own; then the team finds the largest head, and the lowest
+// lane that has it gives it up; which expert it was is looked up for all at the end.
+// Without CHECK, n = k. With it an order may be off by tol + 8 u |order|: n is the first place
+// from k on at which all that follow are certainly less (0 if that is not within L lanes), and
+// `close` is set where neighbours among the n may stand in the wrong order.
+template <bool CHECK, typename K, int L, int V>
+__device__ __forceinline__ int best_experts(const Routing& r, const Team<L>& team,
+                                            const Groups<L, V>& groups, unsigned stay,
+                                            const K (&order)[V], K tol, int& n, bool& close) {
+  using U = decltype(ordered(K()));
+  U key[V], head[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    key[v] = team.rank * V + v < r.E && groups.stays(stay, v) ? ordered(order[v]) : (U)0;
+    head[v] = key[v];
+  }
+  sort_down(head);
+  U my_key = 0, last_key = 0;
+  int my_src = team.base, my_nth = 0, last_src = -1, nth = 0, j = 0;
+  for (;; ++j) {
+    if (!CHECK && j == r.k) break;
+    const U m = team.max(head[0]);
+    if (CHECK) {
+      if (j >= r.k && m == 0) break;  // none left
+      if (j > 0) {
+        const float before = unordered((uint32_t)last_key);
+        const bool far = before - unordered((uint32_t)m) > 2.f * (float)tol + 0x1p-20f * fabsf(before);
+        if (j >= r.k && far) break;
+        if (!far) close = true;
+        if (j == L) {
+          j = 0;
+          break;
+        }
+      }
+    }
+    const int src = __ffs(__ballot_sync(team.mask, head[0] == m)) - 1;
+    nth = m == last_key && src == last_src ? nth + 1 : 0;  // of equal values in one lane
+    last_key = m;
+    last_src = src;
+    if (j == team.rank) {
+      my_key = m;
+      my_src = src;
+      my_nth = nth;
+    }
+    if ((int)(threadIdx.x & 31) == src) {
+#pragma unroll
+      for (int v = 0; v + 1 < V; ++v) head[v] = head[v + 1];
+      head[V - 1] = 0;
+    }
+  }
+  n = j;
+  int at = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (__shfl_sync(team.mask, key[v], my_src) == my_key && my_nth-- == 0) at = v;
+  return (my_src - team.base) * V + at;
+}
+
+// log-free softmax denominator in double: sum of exp(l - mx) over the experts.
+template <int L, int V>
+__device__ __forceinline__ double sum_in_double(const Team<L>& team, const float (&l)[V], float mx) {
+  double total = 0.0;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    if (l[v] > -INFINITY) total += exp((double)l[v] - (double)mx);
+  return team.sum(total);
+}
+
+// The choice with all values in double. Apart from the kernel, whose registers it would
+// crowd.
 template <typename T, int L, int V>
-__device__ __noinline__ int choose_in_double(const Routing r, const T* row, const float* bias) {
+__device__ __noinline__ int choose_in_double(const Routing r, const T* row, const float* bias,
+                                             double* shared) {
   const Team<L> team;
-  const int gs = r.E / r.groups;
+  const Groups<L, V> groups(r, team);
   float l[V];
-  double key[V];
   load_logits<T, V>(row, team.rank, r.E, false, l);
   float mx = -INFINITY;
 #pragma unroll
   for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
   mx = team.max(mx);
-  double total = 1.0;
-  if (!r.sigmoid) {
-    total = 0.0;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (l[v] > -INFINITY) total += exp((double)l[v] - (double)mx);
-    total = team.sum(total);
-    if (total == 0.0) total = 1.0;  // no expert has a score
-  }
-  unsigned open = 0;  // experts of this lane that may still be chosen
+  const double total = r.sigmoid ? 1.0 : sum_in_double(team, l, mx);
+  double value[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = team.rank * V + v;
-    if (e >= r.E) continue;
-    open |= 1u << v;
-    key[v] = l[v] == -INFINITY ? 0.0
-             : r.sigmoid       ? 1.0 / (1.0 + exp(-(double)l[v]))
-                               : exp((double)l[v] - (double)mx) / total;
-    if (bias) key[v] += (double)__ldg(bias + e);
-    if (!(key[v] == key[v])) key[v] = -INFINITY;
-  }
-  if (r.groups > 1) {
-    constexpr int kSlots = (32 + L - 1) / L;
-    double value[kSlots];  // group g's value in lane g % L, slot g / L
-#pragma unroll
-    for (int q = 0; q < kSlots; ++q) value[q] = -INFINITY;
-    for (int g = 0; g < r.groups; ++g) {
-      unsigned left = open;
-      double sum = 0.0;
-      for (int m = 0; m < r.group_top; ++m) {
-        double k1 = -INFINITY;
-        int at = kNone;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int e = team.rank * V + v;
-          if ((left >> v & 1u) && e / gs == g && (at == kNone || key[v] > k1)) {
-            k1 = key[v];
-            at = e;
-          }
-        }
-        team.best(k1, at);
-        sum += k1;
-        if (at / V == team.rank) left &= ~(1u << (at % V));
-      }
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q)
-        if (g == q * L + team.rank) value[q] = sum;
+    value[v] = 0.0;
+    if (l[v] > -INFINITY)
+      value[v] = r.sigmoid ? 1.0 / (1.0 + exp(-(double)l[v])) : exp((double)l[v] - (double)mx) / total;
+    if (bias) {
+      value[v] += e < r.E ? (double)__ldg(bias + e) : 0.0;
+      if (!(value[v] == value[v])) value[v] = -INFINITY;
+    } else if (r.group_top == 1) {
+      value[v] = l[v];
     }
-    unsigned stay = 0;  // groups, the same in every lane
-    for (int m = 0; m < r.topk_groups; ++m) {
-      double k1 = -INFINITY;
-      int at = kNone;
-#pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
-        const int g = q * L + team.rank;
-        if (g < r.groups && !(stay >> g & 1u) && (at == kNone || value[q] > k1)) {
-          k1 = value[q];
-          at = g;
-        }
-      }
-      team.best(k1, at);
-      stay |= 1u << at;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if ((open >> v & 1u) && !(stay >> ((team.rank * V + v) / gs) & 1u)) open &= ~(1u << v);
   }
-  if (!bias) {  // the logits order the experts
+  bool close = false;
+  int n = 0;
+  unsigned stay = 0xffffffffu;
+  if (r.groups > 1) stay = open_groups<false>(r, team, groups, value, 0.0, shared, close);
+  if (!bias) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = l[v];
+    for (int v = 0; v < V; ++v) value[v] = l[v];
   }
-  int mine = -1;
-  for (int j = 0; j < r.k; ++j) {
-    double k1 = -INFINITY;
-    int at = kNone;
+  return best_experts<false>(r, team, groups, stay, value, 0.0, n, close);
+}
+
+// Puts n candidates, one to a lane, in the order of their s + bias in double. Returns the
+// lane's expert in the new order.
+template <typename T, int L, int V>
+__device__ __noinline__ int reorder_in_double(const Routing r, const T* row, const float* bias, int mine,
+                                              int n, int* shared) {
+  const Team<L> team;
+  double total = 1.0;
+  float mx = 0.f;
+  if (!r.sigmoid) {
+    float l[V];
+    load_logits<T, V>(row, team.rank, r.E, false, l);
+    mx = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if ((open >> v & 1u) && (at == kNone || key[v] > k1)) {
-        k1 = key[v];
-        at = team.rank * V + v;
-      }
-    team.best(k1, at);
-    if (at / V == team.rank) open &= ~(1u << (at % V));
-    if (j == team.rank) mine = at;
+    for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
+    mx = team.max(mx);
+    total = sum_in_double(team, l, mx);
   }
-  return mine;
+  const bool in = team.rank < n;
+  double c = -INFINITY;
+  if (in) {
+    const float l = clean(logit_at(row + mine)), b = bias[mine];
+    c = 0.0;
+    if (l > -INFINITY) c = r.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)mx) / total;
+    c += (double)b;
+    if (!(c == c)) c = -INFINITY;
+  }
+  int above = 0;
+  for (int j = 0; j < n; ++j) {
+    const double other = team.from(c, j);
+    const int e = team.from(mine, j);
+    above += other > c || (other == c && e < mine);
+  }
+  __syncwarp(team.mask);
+  if (in) shared[above] = mine;
+  __syncwarp(team.mask);
+  return in ? shared[team.rank] : mine;
 }
 
 // Routing, one team of L lanes per token. The logits alone decide where nothing else is
 // asked for (both scores rise with the logit, so fp32 is exact); else the values s + bias
-// and the groups' sums are formed in fp32, and a token two of whose compared values lie
-// within the sums of their error bounds is chosen again in double (about one token in
-// a thousand): fp32 work, decisions as in double. Bounds, u = 2^-24: a sigmoid is off by
-// 4u (exponential, two ulp) + 2u, a softmax by at most 32u of the largest probability
-// (exponential 4u, its argument's rounding, a sum of up to 512 terms in a tree, a
-// division), and the sum with the bias by u of its value.
+// and the groups' sums are formed in fp32 with the fast exponential and division, and what
+// lies within its error bounds of a decision is decided in double: the order of the
+// candidates from their own values (one a lane), the groups and long rows of ties from
+// all values. Bounds, with u = 2^-24: the exponential is off by 2 + 1.2 |x| ulp, the
+// division by 2 ulp; x e^-x is at most 0.37, so a sigmoid is off by less than 5 u (8 u are
+// allowed), a softmax by less than 32 u of the largest probability (its sum of up to 512 terms
+// is a tree of 20 levels), and the sum with the bias by u of its value.
 //
-// The k largest are taken one by one: each lane keeps the largest of its own values, the
-// team finds the largest of those, the lowest lane that has it gives its lowest expert.
-// Bound by instructions, not bytes: a team is as narrow as 8 values per lane allow, so
-// that a warp's instruction serves up to four tokens.
+// Bound by instructions, not bytes: a team is as narrow as 16 values per lane allow, so that
+// a warp's instruction serves up to four tokens.
 template <typename T, int L, int V>
-__global__ void __launch_bounds__(32 * kWarps) k_route(const Routing r, const T* __restrict__ logits,
-                                                       const float* __restrict__ bias, int vec,
-                                                       int32_t* __restrict__ idx_out,
-                                                       float* __restrict__ w_out) {
+__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
+    k_route(const Routing r, const T* __restrict__ logits, const float* __restrict__ bias, int vec,
+            int32_t* __restrict__ idx_out, float* __restrict__ w_out) {
   pdl_trigger();
   pdl_wait();
-  __shared__ float s_value[kWarps * 32 / L][L * V + 1];
+  __shared__ double s_value[kWarps * 32 / L][L * V + L * V / 32 + 1];
+  __shared__ __align__(16) float s_bias[L * V];
   const Team<L> team;
+  const Groups<L, V> groups(r, team);
   constexpr int kPer = 32 / L * kWarps;  // tokens per block
-  float* value_of = s_value[threadIdx.x / L];
-  const int gs = r.E / r.groups;
-  const bool grouped = r.groups > 1;
+  double* shared = s_value[threadIdx.x / L];
   const bool scores = bias || r.group_top > 1;
-  // lanes of a group: a power of two, so that they can reduce among themselves
-  int lanes = L;
-  while (lanes * r.groups > L) lanes >>= 1;
-  const bool narrow = lanes > 0 && r.group_top <= 2;
-  int bit[V];  // of each of the lane's experts' groups in `stay`
-#pragma unroll
-  for (int v = 0; v < V; ++v) bit[v] = grouped ? team.base + (team.rank * V + v) / gs * lanes : 0;
+  int pairs = 1;  // lanes up to the next power of two of k: the slots' reductions
+  while (pairs < r.k) pairs *= 2;
+  if (bias) {
+    for (int e = threadIdx.x; e < L * V; e += 32 * kWarps) {
+      const float b = e < r.E ? __ldg(bias + e) : 0.f;
+      s_bias[e] = b == b ? b : -INFINITY;
+    }
+    __syncthreads();
+  }
   for (int64_t t0 = (int64_t)blockIdx.x * kPer; t0 < r.T; t0 += (int64_t)gridDim.x * kPer) {
     const int64_t t = t0 + threadIdx.x / L;
     if (t >= r.T) continue;  // a token's lanes leave together
     const T* row = logits + t * r.stride;
     float l[V], c[V];
     load_logits<T, V>(row, team.rank, r.E, vec, l);
-    float mx = -INFINITY, tol = 0.f, sum = 1.f;
+    float mx = -INFINITY, tol = 0.f;
     if (!r.sigmoid && (scores || !r.renorm)) {
 #pragma unroll
       for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
       mx = team.max(mx);
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = l[v];
     if (scores) {
       if (r.sigmoid) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) c[v] = l[v] > -INFINITY ? 1.f / (1.f + expf(-l[v])) : 0.f;
-        tol = 0x1p-20f;
+        for (int v = 0; v < V; ++v) c[v] = __fdividef(1.f, 1.f + __expf(-l[v]));
+        tol = 0x1p-21f;
       } else {
-        sum = 0.f;
+        float sum = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          c[v] = l[v] > -INFINITY ? expf(l[v] - mx) : 0.f;
+          c[v] = l[v] > -INFINITY ? __expf(l[v] - mx) : 0.f;
           sum += c[v];
         }
         sum = team.sum(sum);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) c[v] *= inv;
-        tol = 0x1p-18f * inv;  // the largest probability is 1 / sum
+        tol = 0x1p-19f * inv;  // the largest probability is 1 / sum
       }
       if (bias) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int e = team.rank * V + v;
-          if (e < r.E) c[v] += __ldg(bias + e);
-          if (!(c[v] == c[v])) c[v] = -INFINITY;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int v = 0; v < V; ++v) c[v] = l[v];
-    }
-    bool close = false;
-    unsigned stay = 0xffffffffu;  // bit base + g * lanes: group g stays
-    if (grouped) {
-      close = !narrow;
-      if (narrow) {
-        __syncwarp(team.mask);
-#pragma unroll
-        for (int v = 0; v < V; ++v) value_of[team.rank * V + v] = c[v];
-        __syncwarp(team.mask);
-        const int g = team.rank / lanes;
-        float m1 = -INFINITY, m2 = -INFINITY;
-        if (g < r.groups) {
-          for (int i = team.rank - g * lanes; i < gs; i += lanes) {
-            const float v = value_of[g * gs + i];
-            m2 = fmaxf(m2, fminf(v, m1));
-            m1 = fmaxf(m1, v);
-          }
-        }
-        for (int o = lanes >> 1; o > 0; o >>= 1) {
-          const float o1 = __shfl_xor_sync(team.mask, m1, o), o2 = __shfl_xor_sync(team.mask, m2, o);
-          m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
-          m1 = fmaxf(m1, o1);
-        }
-        const float value = r.group_top == 2 ? m1 + m2 : m1;
-        // what the group's value may be off by: its terms' bounds and their sum's rounding
-        const float off = 2.f * tol + 0x1p-21f * (fabsf(m1) + (r.group_top == 2 ? fabsf(m2) : 0.f));
-        int above = 0;
-        for (int j = 0; j < r.groups; ++j) {
-          const float other = team.from(value, j * lanes);
-          above += other > value || (other == value && j < g);
-          if (scores) {
-            const float reach = off + team.from(off, j * lanes);
-            if (j != g && g < r.groups && !(fabsf(other - value) > reach)) close = true;
-          }
-        }
-        stay = __ballot_sync(team.mask, above < r.topk_groups);
-        close = __any_sync(team.mask, close);
+        for (int v = 0; v < V; ++v) c[v] += s_bias[team.rank * V + v];
       }
     }
-    int mine = -1;
+    bool close = r.group_top > 2;
+    int mine = 0, n = 0;
+    unsigned stay = 0xffffffffu;
+    if (r.groups > 1 && !close) {
+      bool near = false;
+      stay = open_groups<true>(r, team, groups, c, tol, reinterpret_cast<float*>(shared), near);
+      close = scores && near;
+    }
     if (!close) {
-      uint32_t key[V], top = 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = team.rank * V + v;
-        const bool open = e < r.E && (!grouped || (stay >> bit[v] & 1u));
-        key[v] = open ? ordered(bias ? c[v] : l[v]) : 0u;
-        top = key[v] > top ? key[v] : top;
-      }
-      float before = 0.f;
-      const int passes = bias ? r.k + 1 : r.k;  // one more to see how far the next one is
-      for (int j = 0; j < passes; ++j) {
-        const uint32_t m = team.max(top);
-        if (bias) {
-          const float now = unordered(m);
-          if (j > 0 && m != 0 && !(before - now > 2.f * tol + 0x1p-21f * fabsf(before))) close = true;
-          before = now;
-          if (j == r.k) break;
-        }
-        const int src = __ffs(__ballot_sync(team.mask, top == m)) - 1;
-        int e = 0;
-        if ((int)(threadIdx.x & 31) == src) {
-          int at = 0;
-#pragma unroll
-          for (int v = V - 1; v >= 0; --v)
-            if (key[v] == m) at = v;
-          top = 0;
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            if (v == at) key[v] = 0;
-            top = key[v] > top ? key[v] : top;
-          }
-          e = team.rank * V + at;
-        }
-        e = __shfl_sync(team.mask, e, src);
-        if (j == team.rank) mine = e;
+      if (bias) {
+        bool near = false;
+        mine = best_experts<true>(r, team, groups, stay, c, tol, n, near);
+        close = n == 0;
+        if (near && !close) mine = reorder_in_double<T, L, V>(r, row, bias, mine, n, reinterpret_cast<int*>(shared));
+      } else {
+        bool near = false;
+        mine = best_experts<false>(r, team, groups, stay, l, 0.f, n, near);
       }
     }
-    if (close) mine = choose_in_double<T, L, V>(r, row, bias);
+    if (close) mine = choose_in_double<T, L, V>(r, row, bias, shared);
     // weights: one lane per slot, in double, rounded once
     const bool slot = team.rank < r.k;
     const float ls = slot ? clean(logit_at(row + mine)) : -INFINITY;
@@ -393,18 +544,17 @@ __global__ void __launch_bounds__(32 * kWarps) k_route(const Routing r, const T*
     if (r.sigmoid) {
       if (ls > -INFINITY) s = 1.0 / (1.0 + exp(-(double)ls));
     } else if (r.renorm) {  // the sum over all experts cancels
-      const float most = team.max(ls);
+      float most = ls;
+      for (int o = pairs >> 1; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(team.mask, most, o));
       if (ls > -INFINITY) s = exp((double)ls - (double)most);
     } else {
-      double total = 0.0;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (l[v] > -INFINITY) total += exp((double)l[v] - (double)mx);
-      total = team.sum(total);
+      load_logits<T, V>(row, team.rank, r.E, vec, l);
+      const double total = sum_in_double(team, l, mx);
       if (ls > -INFINITY) s = exp((double)ls - (double)mx) / total;
     }
     if (r.renorm) {
-      const double all = team.sum(s);
+      double all = s;
+      for (int o = pairs >> 1; o > 0; o >>= 1) all += __shfl_xor_sync(team.mask, all, o);
       s = all > 0.0 ? s / all : 0.0;
     }
     if (slot) {
@@ -457,7 +607,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_losses(const Routing r, const T
       sum = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        x[v] = l[v] > -INFINITY ? 1.f / (1.f + expf(-l[v])) : 0.f;
+        float rest;
+        sigmoid_pair(l[v], x[v], rest);
         sum += x[v];
       }
       sum = team.sum(sum);
@@ -561,11 +712,13 @@ __global__ void __launch_bounds__(32 * kWarps)
     k_route_bwd(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
                 const float* __restrict__ d_w, const int32_t* __restrict__ counts,
                 const float* __restrict__ d_losses, const uint8_t* __restrict__ mask, int vec,
-                T* __restrict__ d_logits) {
+                int vec_out, T* __restrict__ d_logits) {
   pdl_trigger();
   pdl_wait();
   const Team<L> team;
   constexpr int kPer = 32 / L * kWarps;
+  __shared__ __align__(16) float s_slots[kWarps * 32 / L][L * V];
+  float* slots = s_slots[threadIdx.x / L];
   float c[V], zc = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) c[v] = 0.f;
@@ -623,17 +776,18 @@ __global__ void __launch_bounds__(32 * kWarps)
         float s[V], sum = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          s[v] = l[v] > -INFINITY ? 1.f / (1.f + expf(-l[v])) : 0.f;
+          float rest;
+          sigmoid_pair(l[v], s[v], rest);
           sum += s[v];
           cs += c[v] * s[v];
+          dl[v] = s[v] * rest;
         }
         sum = team.sum(sum);
         const float inv = sum > 0.f ? 1.f / sum : 0.f;
         cs = team.sum(cs) * inv;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float rest = l[v] > -INFINITY ? 1.f / (1.f + expf(l[v])) : 0.f;  // 1 - s
-          dl[v] = s[v] * rest * (c[v] - cs) * inv + zc * lse * p[v];
+          dl[v] = dl[v] * (c[v] - cs) * inv + zc * lse * p[v];
         }
       } else {
 #pragma unroll
@@ -646,10 +800,7 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (d_w) {
       float u = 0.f, rest = 1.f;
       if (r.sigmoid) {
-        if (my_e >= 0 && ls > -INFINITY) {
-          u = 1.f / (1.f + expf(-ls));
-          rest = 1.f / (1.f + expf(ls));
-        }
+        if (my_e >= 0) sigmoid_pair(ls, u, rest);
       } else if (r.renorm) {
         const float top = team.max(ls);
         if (ls > -INFINITY) u = expf(ls - top);
@@ -669,19 +820,17 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
         for (int v = 0; v < V; ++v) dl[v] -= p[v] * gp;
       }
-      for (int j = 0; j < r.k; ++j) {
-        const int e = team.from(my_e, j);
-        const float add = team.from(term, j);
+      // from the slots' lanes to their experts'
+      __syncwarp(team.mask);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (e == team.rank * V + v) dl[v] += add;
-      }
-    }
+      for (int v = 0; v < V; ++v) slots[team.rank * V + v] = 0.f;
+      __syncwarp(team.mask);
+      if (my_e >= 0) atomicAdd(slots + my_e, term);
+      __syncwarp(team.mask);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = team.rank * V + v;
-      if (e < r.E) store(d_logits + t * r.E + e, dl[v]);
+      for (int v = 0; v < V; ++v) dl[v] += slots[team.rank * V + v];
     }
+    store_row<T, V>(d_logits + t * r.E, team.rank, r.E, vec_out, dl);
   }
 }
 
@@ -698,9 +847,28 @@ cudaError_t with(F f) {
   return f(std::integral_constant<int, L>(), std::integral_constant<int, V>());
 }
 
+// Routing: a lane per slot, and one per group at least.
+template <typename F>
+cudaError_t by_choice(const Routing& r, F f) {
+  if (r.k <= 8 && r.groups <= 8) {
+    if (r.E <= 8) return with<8, 1>(f);
+    if (r.E <= 16) return with<8, 2>(f);
+    if (r.E <= 32) return with<8, 4>(f);
+    if (r.E <= 64) return with<8, 8>(f);
+    if (r.E <= 128) return with<8, 16>(f);
+    if (r.E <= 256) return with<16, 16>(f);
+  } else {
+    if (r.E <= 64) return with<32, 2>(f);
+    if (r.E <= 128) return with<32, 4>(f);
+    if (r.E <= 256) return with<32, 8>(f);
+  }
+  return with<32, 16>(f);
+}
+
+// Losses and gradient: a lane per slot.
 template <typename F>
 cudaError_t by_sizes(const Routing& r, F f) {
-  if (r.k <= 8 && r.groups <= 8) {  // a lane per slot, and one per group at least
+  if (r.k <= 8) {
     if (r.E <= 8) return with<8, 1>(f);
     if (r.E <= 16) return with<8, 2>(f);
     if (r.E <= 32) return with<8, 4>(f);
@@ -714,29 +882,29 @@ cudaError_t by_sizes(const Routing& r, F f) {
   return with<32, 16>(f);
 }
 
-// Whether every lane's V logits start on a boundary of their size (16 bytes at most).
+// Whether every lane's V values start on a boundary of their size (16 bytes at most).
 template <typename T, int V>
-int vectors(const Routing& r, const T* logits) {
+int vectors(const Routing& r, const T* p, int64_t stride) {
   constexpr size_t kBytes = V * sizeof(T) < 16 ? V * sizeof(T) : 16;
-  return r.E % V == 0 && reinterpret_cast<uintptr_t>(logits) % kBytes == 0 &&
-         (r.T == 1 || r.stride * (int64_t)sizeof(T) % (int64_t)kBytes == 0);
+  return r.E % V == 0 && reinterpret_cast<uintptr_t>(p) % kBytes == 0 &&
+         (r.T == 1 || stride * (int64_t)sizeof(T) % (int64_t)kBytes == 0);
 }
 
 }  // namespace
 
 cudaError_t launch_route(const Routing& r, const void* logits, const float* bias, int32_t* idx,
                          float* w, cudaStream_t st) {
-  return by_sizes(r, [&](auto l, auto v) {
+  return by_choice(r, [&](auto l, auto v) {
     constexpr int L = decltype(l)::value, V = decltype(v)::value;
-    const dim3 grid(token_blocks<L>(r, 8)), block(32 * kWarps);
+    const dim3 grid(token_blocks<L>(r, V <= 8 ? 3 : 2)), block(32 * kWarps);
     if (r.bf16) {
       const auto* p = static_cast<const __nv_bfloat16*>(logits);
       return launch_pdl(k_route<__nv_bfloat16, L, V>, grid, block, 0, st, r, p, bias,
-                        vectors<__nv_bfloat16, V>(r, p), idx, w);
+                        vectors<__nv_bfloat16, V>(r, p, r.stride), idx, w);
     }
     const auto* p = static_cast<const float*>(logits);
     return launch_pdl(k_route<float, L, V>, grid, block, 0, st, r, p, bias,
-                      vectors<float, V>(r, p), idx, w);
+                      vectors<float, V>(r, p, r.stride), idx, w);
   });
 }
 
@@ -761,11 +929,11 @@ cudaError_t launch_router_losses(const Routing& r, const void* logits, const int
       if (r.bf16) {
         const auto* p = static_cast<const __nv_bfloat16*>(logits);
         return launch_pdl(k_losses<__nv_bfloat16, L, V>, grid, block, 0, st, r, p, idx, mask,
-                          vectors<__nv_bfloat16, V>(r, p), part_sum, part_count);
+                          vectors<__nv_bfloat16, V>(r, p, r.stride), part_sum, part_count);
       }
       const auto* p = static_cast<const float*>(logits);
       return launch_pdl(k_losses<float, L, V>, grid, block, 0, st, r, p, idx, mask,
-                        vectors<float, V>(r, p), part_sum, part_count);
+                        vectors<float, V>(r, p, r.stride), part_sum, part_count);
     });
     if (e != cudaSuccess) return e;
   }
@@ -782,12 +950,15 @@ cudaError_t launch_route_backward(const Routing& r, const void* logits, const in
     if (r.bf16) {
       const auto* p = static_cast<const __nv_bfloat16*>(logits);
       return launch_pdl(k_route_bwd<__nv_bfloat16, L, V>, grid, block, 0, st, r, p, idx, d_w, counts,
-                        d_losses, mask, vectors<__nv_bfloat16, V>(r, p),
+                        d_losses, mask, vectors<__nv_bfloat16, V>(r, p, r.stride),
+                        vectors<__nv_bfloat16, V>(r, static_cast<__nv_bfloat16*>(d_logits), r.E),
                         static_cast<__nv_bfloat16*>(d_logits));
     }
     const auto* p = static_cast<const float*>(logits);
     return launch_pdl(k_route_bwd<float, L, V>, grid, block, 0, st, r, p, idx, d_w, counts, d_losses,
-                      mask, vectors<float, V>(r, p), static_cast<float*>(d_logits));
+                      mask, vectors<float, V>(r, p, r.stride),
+                      vectors<float, V>(r, static_cast<float*>(d_logits), r.E),
+                      static_cast<float*>(d_logits));
   });
 }
 
