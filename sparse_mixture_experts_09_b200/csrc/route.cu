@@ -61,18 +61,6 @@ struct Team {
     for (int o = L / 2; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(mask, v, o));
     return v;
   }
-  __device__ uint32_t max(uint32_t v) const {
-    if constexpr (L == 32) {
-      return __reduce_max_sync(0xffffffffu, v);
-    } else {
-#pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) {
-        const uint32_t w = __shfl_xor_sync(mask, v, o);
-        v = w > v ? w : v;
-      }
-      return v;
-    }
-  }
   __device__ unsigned long long max(unsigned long long v) const {
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) {
@@ -157,37 +145,39 @@ __device__ __forceinline__ void store_row(T* row, int rank, int E, bool vec, con
   }
 }
 
-// Floats and doubles as unsigned numbers of the same order (-0 as +0); all are above 0.
-__device__ __forceinline__ uint32_t ordered(float f) {
-  const uint32_t u = __float_as_uint(f + 0.f);
-  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-}
+// Doubles as unsigned numbers of the same order (-0 as +0); all are above 0.
 __device__ __forceinline__ unsigned long long ordered(double f) {
   const unsigned long long u = (unsigned long long)__double_as_longlong(f + 0.0);
   return u ^ ((unsigned long long)((long long)u >> 63) | 0x8000000000000000ull);
 }
-__device__ __forceinline__ float unordered(uint32_t u) {
-  return __uint_as_float(u ^ ((uint32_t)((int32_t)~u >> 31) | 0x80000000u));
-}
 
-template <typename U>
-__device__ __forceinline__ void in_order(U& a, U& b) {  // the larger first
-  const U hi = a > b ? a : b;
-  b = a > b ? b : a;
-  a = hi;
+// 2^x to within 2^-22 of the value, and 1 / x to within one ulp (subnormals as 0).
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Descending, by Batcher's odd-even merge (all indices are known at compile time).
-template <typename U, int V>
-__device__ __forceinline__ void sort_down(U (&a)[V]) {
+template <int V>
+__device__ __forceinline__ void sort_down(float (&a)[V]) {
 #pragma unroll
   for (int p = 1; p < V; p *= 2)
 #pragma unroll
     for (int k = p; k >= 1; k /= 2)
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (i >= k % p && (i - k % p) % (2 * k) < k && i + k < V && i / (2 * p) == (i + k) / (2 * p))
-          in_order(a[i], a[i + k]);
+        if (i >= k % p && (i - k % p) % (2 * k) < k && i + k < V && i / (2 * p) == (i + k) / (2 * p)) {
+          const float hi = fmaxf(a[i], a[i + k]);
+          a[i + k] = fminf(a[i], a[i + k]);
+          a[i] = hi;
+        }
 }
 
 // How a team's lanes share the groups: `lanes` of them (a power of two) to a group.
@@ -300,43 +290,44 @@ __device__ __forceinline__ unsigned open_groups(const Routing& r, const Team<L>&
   return __ballot_sync(team.mask, in);
 }
 
-// The best experts in order, one to a lane: order[v] compares them. Returns the expert of lane
-// `rank` below n. Each lane sorts its own; then the team finds the largest head, and the lowest
-// lane that has it gives it up; which expert it was is looked up for all at the end.
-// Without CHECK, n = k. With it an order may be off by tol + 8 u |order|: n is the first place
-// from k on at which all that follow are certainly less (0 if that is not within L lanes), and
-// `close` is set where neighbours among the n may stand in the wrong order.
-template <bool CHECK, typename K, int L, int V>
-__device__ __forceinline__ int best_experts(const Routing& r, const Team<L>& team,
-                                            const Groups<L, V>& groups, unsigned stay,
-                                            const K (&order)[V], K tol, int& n, bool& close) {
-  using U = decltype(ordered(K()));
-  U key[V], head[V];
+// The best experts in order, one to a lane; order[v] compares them, -inf is none. Returns
+// the expert of lane `rank` below n. Each lane sorts its own and lays them out in shared memory;
+// then the team finds the largest head, and the lowest lane that has it gives it up; which
+// expert it was is looked up for all at the end. n = k where the order is exact (tol < 0). Else an
+// order may be off by tol + 8 u |order|: n is the first place from k on at which all that
+// follow are certainly less, and `close` is set where neighbours among the n may stand in
+// the wrong order. n = 0: not to be had this way (fewer than k finite values, or a run of
+// near ties longer than the team).
+template <int L, int V>
+__device__ __forceinline__ int best_experts(const Routing& r, const Team<L>& team, const float (&order)[V],
+                                            float tol, float* shared, int& n, bool& close) {
+  float sorted[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    key[v] = team.rank * V + v < r.E && groups.stays(stay, v) ? ordered(order[v]) : (U)0;
-    head[v] = key[v];
-  }
-  sort_down(head);
-  U my_key = 0, last_key = 0;
-  int my_src = team.base, my_nth = 0, last_src = -1, nth = 0, j = 0;
+  for (int v = 0; v < V; ++v) sorted[v] = order[v];
+  sort_down(sorted);
+  __syncwarp(team.mask);
+#pragma unroll
+  for (int v = 1; v < V; ++v) shared[v * L + team.rank] = sorted[v];
+  float head = sorted[0], my_key = 0.f, last_key = INFINITY;
+  int next = 1, my_src = team.base, my_nth = 0, last_src = -1, nth = 0, j = 0;
+  const float reach = 2.f * tol;
   for (;; ++j) {
-    if (!CHECK && j == r.k) break;
-    const U m = team.max(head[0]);
-    if (CHECK) {
-      if (j >= r.k && m == 0) break;  // none left
-      if (j > 0) {
-        const float before = unordered((uint32_t)last_key);
-        const bool far = before - unordered((uint32_t)m) > 2.f * (float)tol + 0x1p-20f * fabsf(before);
-        if (j >= r.k && far) break;
-        if (!far) close = true;
-        if (j == L) {
-          j = 0;
-          break;
-        }
+    if (tol < 0.f && j == r.k) break;
+    const float m = team.max(head);
+    if (m == -INFINITY) {
+      if (j < r.k) j = 0;
+      break;
+    }
+    if (tol >= 0.f && j > 0) {
+      const bool far = last_key - m > reach + 0x1p-20f * fabsf(last_key);
+      if (j >= r.k && far) break;
+      if (!far) close = true;
+      if (j == L) {
+        j = 0;
+        break;
       }
     }
-    const int src = __ffs(__ballot_sync(team.mask, head[0] == m)) - 1;
+    const int src = __ffs(__ballot_sync(team.mask, head == m)) - 1;
     nth = m == last_key && src == last_src ? nth + 1 : 0;  // of equal values in one lane
     last_key = m;
     last_src = src;
@@ -346,20 +337,135 @@ __device__ __forceinline__ int best_experts(const Routing& r, const Team<L>& tea
       my_nth = nth;
     }
     if ((int)(threadIdx.x & 31) == src) {
-#pragma unroll
-      for (int v = 0; v + 1 < V; ++v) head[v] = head[v + 1];
-      head[V - 1] = 0;
+      head = next < V ? shared[next * L + team.rank] : -INFINITY;
+      ++next;
     }
   }
   n = j;
   int at = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (__shfl_sync(team.mask, key[v], my_src) == my_key && my_nth-- == 0) at = v;
+    if (__shfl_sync(team.mask, order[v], my_src) == my_key && my_nth-- == 0) at = v;
   return (my_src - team.base) * V + at;
 }
 
-// log-free softmax denominator in double: sum of exp(l - mx) over the experts.
+// As best_experts for k <= 8, without its k rounds in a row: the lanes' sorted lists, cut to 8,
+// are merged in log2 L steps (of two descending lists the larger of each pair a[i], b[7 - i] is
+// the best 8, and three exchange stages sort them), the k-th value marks the candidates, a
+// prefix sum gives each a lane, and a candidate's slot is the number of those above it.
+// Returns the lane's candidate; slot < k where it is chosen. `unsure` (a team's lanes agree): the
+// choice is not to be had this way.
+template <int L, int V>
+__device__ __forceinline__ int best_few(const Routing& r, const Team<L>& team, const float (&order)[V],
+                                        float tol, float2* shared, float& value, int& n, int& slot,
+                                        bool& close, bool& unsure) {
+  int mine = team.rank;
+  value = order[0];
+  n = L;
+  if constexpr (V > 1) {
+    float sorted[V], top[8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) sorted[v] = order[v];
+    sort_down(sorted);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[i] = i < V ? sorted[i < V ? i : 0] : -INFINITY;
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+      float other[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(team.mask, top[i], o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top[i] = fmaxf(top[i], other[7 - i]);
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!(i & d)) {
+            const float hi = fmaxf(top[i], top[i + d]);
+            top[i + d] = fminf(top[i], top[i + d]);
+            top[i] = hi;
+          }
+    }
+    float last = top[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) last = i < r.k ? top[i] : last;
+    if (last == -INFINITY) {  // fewer than k finite values
+      unsure = true;
+      return 0;
+    }
+    const float low = tol < 0.f ? last : last - (2.f * tol + 0x1p-20f * fabsf(last));
+    int count = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) count += order[v] >= low;
+    int upto = count;
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+      const int before = __shfl_up_sync(team.mask, upto, o, L);
+      if (team.rank >= o) upto += before;
+    }
+    n = team.from(upto, L - 1);
+    if (n > L) {
+      unsure = true;
+      return 0;
+    }
+    __syncwarp(team.mask);
+    int at = upto - count;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (order[v] >= low) shared[at++] = make_float2(order[v], __int_as_float(team.rank * V + v));
+    __syncwarp(team.mask);
+    value = -INFINITY;
+    if (team.rank < n) {
+      const float2 got = shared[team.rank];
+      value = got.x;
+      mine = __float_as_int(got.y);
+    }
+  }
+  slot = 0;
+  bool near = false;
+  const float reach = 2.f * tol + 0x1p-20f * fabsf(value);
+  for (int j = 0; j < n; ++j) {
+    const float other = team.from(value, j);
+    slot += other > value || (other == value && j < team.rank);
+    near |= j != team.rank && !(fabsf(other - value) > reach);
+  }
+  close = tol >= 0.f && __any_sync(team.mask, near && slot < r.k);
+  if (V == 1) unsure = __any_sync(team.mask, slot < r.k && value == -INFINITY);
+  return mine;
+}
+
+// The k best of the open groups by their values in double: lane j < k returns its expert.
+template <int L, int V>
+__device__ __forceinline__ int best_in_double(const Routing& r, const Team<L>& team,
+                                              const Groups<L, V>& groups, unsigned stay,
+                                              const double (&order)[V]) {
+  unsigned long long key[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    key[v] = team.rank * V + v < r.E && groups.stays(stay, v) ? ordered(order[v]) : 0ull;
+  int mine = 0;
+  for (int j = 0; j < r.k; ++j) {
+    unsigned long long top = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) top = key[v] > top ? key[v] : top;
+    const unsigned long long m = team.max(top);
+    const int src = __ffs(__ballot_sync(team.mask, top == m)) - 1;
+    int at = 0;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v)
+      if (key[v] == m) at = v;
+    if ((int)(threadIdx.x & 31) == src) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (v == at) key[v] = 0;
+    }
+    at = __shfl_sync(team.mask, at, src);
+    if (j == team.rank) mine = (src - team.base) * V + at;
+  }
+  return mine;
+}
+
+// The softmax's denominator in double: the sum of exp(l - mx) over the experts.
 template <int L, int V>
 __device__ __forceinline__ double sum_in_double(const Team<L>& team, const float (&l)[V], float mx) {
   double total = 0.0;
@@ -398,21 +504,19 @@ __device__ __noinline__ int choose_in_double(const Routing r, const T* row, cons
     }
   }
   bool close = false;
-  int n = 0;
   unsigned stay = 0xffffffffu;
   if (r.groups > 1) stay = open_groups<false>(r, team, groups, value, 0.0, shared, close);
   if (!bias) {
 #pragma unroll
     for (int v = 0; v < V; ++v) value[v] = l[v];
   }
-  return best_experts<false>(r, team, groups, stay, value, 0.0, n, close);
+  return best_in_double(r, team, groups, stay, value);
 }
 
-// Puts n candidates, one to a lane, in the order of their s + bias in double. Returns the
-// lane's expert in the new order.
+// The place of the lane's candidate among n, one to a lane, by their s + bias in double.
 template <typename T, int L, int V>
 __device__ __noinline__ int reorder_in_double(const Routing r, const T* row, const float* bias, int mine,
-                                              int n, int* shared) {
+                                              int n) {
   const Team<L> team;
   double total = 1.0;
   float mx = 0.f;
@@ -440,25 +544,23 @@ __device__ __noinline__ int reorder_in_double(const Routing r, const T* row, con
     const int e = team.from(mine, j);
     above += other > c || (other == c && e < mine);
   }
-  __syncwarp(team.mask);
-  if (in) shared[above] = mine;
-  __syncwarp(team.mask);
-  return in ? shared[team.rank] : mine;
+  return in ? above : L;
 }
 
 // Routing, one team of L lanes per token. The logits alone decide where nothing else is
 // asked for (both scores rise with the logit, so fp32 is exact); else the values s + bias
-// and the groups' sums are formed in fp32 with the fast exponential and division, and what
+// and the groups' sums are formed in fp32 with the approximate exponential and reciprocal, and what
 // lies within its error bounds of a decision is decided in double: the order of the
-// candidates from their own values (one a lane), the groups and long rows of ties from
-// all values. Bounds, with u = 2^-24: the exponential is off by 2 + 1.2 |x| ulp, the
-// division by 2 ulp; x e^-x is at most 0.37, so a sigmoid is off by less than 5 u (8 u are
-// allowed), a softmax by less than 32 u of the largest probability (its sum of up to 512 terms
-// is a tree of 20 levels), and the sum with the bias by u of its value.
+// candidates from their own values (one a lane), the groups, long rows of ties and rows
+// with fewer than k finite values from all values. Bounds, with u = 2^-24: the exponential is
+// off by 4 u and by 1.5 u |x| for its argument, the reciprocal by 2 u; s (1 - s) is at most
+// 1/4 and |x| s (1 - s) at most 0.23, so a sigmoid is off by less than 5 u (8 u are allowed); |x| e^x
+// is at most 0.37 below 0, so a softmax is off by less than 32 u of the largest probability (its
+// sum of up to 512 terms is a tree of 20 levels); the sum with the bias by u of its value.
 //
 // Bound by instructions, not bytes: a team is as narrow as 16 values per lane allow, so that
 // a warp's instruction serves up to four tokens.
-template <typename T, int L, int V>
+template <typename T, int L, int V, bool FEW>
 __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
     k_route(const Routing r, const T* __restrict__ logits, const float* __restrict__ bias, int vec,
             int32_t* __restrict__ idx_out, float* __restrict__ w_out) {
@@ -475,7 +577,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
   while (pairs < r.k) pairs *= 2;
   if (bias) {
     for (int e = threadIdx.x; e < L * V; e += 32 * kWarps) {
-      const float b = e < r.E ? __ldg(bias + e) : 0.f;
+      const float b = e < r.E ? __ldg(bias + e) : -INFINITY;
       s_bias[e] = b == b ? b : -INFINITY;
     }
     __syncthreads();
@@ -497,17 +599,17 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
     if (scores) {
       if (r.sigmoid) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) c[v] = __fdividef(1.f, 1.f + __expf(-l[v]));
+        for (int v = 0; v < V; ++v) c[v] = fast_rcp(1.f + fast_exp2(-kLog2e * l[v]));
         tol = 0x1p-21f;
       } else {
         float sum = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          c[v] = l[v] > -INFINITY ? __expf(l[v] - mx) : 0.f;
+          c[v] = l[v] > -INFINITY ? fast_exp2(kLog2e * (l[v] - mx)) : 0.f;
           sum += c[v];
         }
         sum = team.sum(sum);
-        const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+        const float inv = sum > 0.f ? fast_rcp(sum) : 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) c[v] *= inv;
         tol = 0x1p-19f * inv;  // the largest probability is 1 / sum
@@ -518,7 +620,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
       }
     }
     bool close = r.group_top > 2;
-    int mine = 0, n = 0;
+    int mine = 0, n = 0, slot = team.rank;
     unsigned stay = 0xffffffffu;
     if (r.groups > 1 && !close) {
       bool near = false;
@@ -527,25 +629,42 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
     }
     if (!close) {
       if (bias) {
-        bool near = false;
-        mine = best_experts<true>(r, team, groups, stay, c, tol, n, near);
-        close = n == 0;
-        if (near && !close) mine = reorder_in_double<T, L, V>(r, row, bias, mine, n, reinterpret_cast<int*>(shared));
-      } else {
-        bool near = false;
-        mine = best_experts<false>(r, team, groups, stay, l, 0.f, n, near);
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = c[v];
       }
+      if (r.groups > 1) {
+        if (groups.size == V * groups.lanes) {  // one group's all
+          const bool open = groups.stays(stay, 0);
+#pragma unroll
+          for (int v = 0; v < V; ++v) l[v] = open ? l[v] : -INFINITY;
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) l[v] = groups.stays(stay, v) ? l[v] : -INFINITY;
+        }
+      }
+      bool near = false;
+      float value;
+      if constexpr (FEW)
+        mine = best_few(r, team, l, bias ? tol : -1.f, reinterpret_cast<float2*>(shared), value, n, slot, near, close);
+      else
+        mine = best_experts(r, team, l, bias ? tol : -1.f, reinterpret_cast<float*>(shared), n, near);
+      if (!FEW) close = n == 0;
+      if (near && !close) slot = reorder_in_double<T, L, V>(r, row, bias, mine, n);
     }
-    if (close) mine = choose_in_double<T, L, V>(r, row, bias, shared);
+    if (close) {
+      mine = choose_in_double<T, L, V>(r, row, bias, shared);
+      slot = team.rank;
+    }
     // weights: one lane per slot, in double, rounded once
-    const bool slot = team.rank < r.k;
-    const float ls = slot ? clean(logit_at(row + mine)) : -INFINITY;
+    const bool chosen = slot < r.k;
+    const float ls = chosen ? clean(logit_at(row + mine)) : -INFINITY;
+    const int reduce = n > pairs ? L : pairs;  // the chosen are among the first lanes
     double s = 0.0;
     if (r.sigmoid) {
       if (ls > -INFINITY) s = 1.0 / (1.0 + exp(-(double)ls));
     } else if (r.renorm) {  // the sum over all experts cancels
       float most = ls;
-      for (int o = pairs >> 1; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(team.mask, most, o));
+      for (int o = reduce >> 1; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(team.mask, most, o));
       if (ls > -INFINITY) s = exp((double)ls - (double)most);
     } else {
       load_logits<T, V>(row, team.rank, r.E, vec, l);
@@ -554,12 +673,12 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
     }
     if (r.renorm) {
       double all = s;
-      for (int o = pairs >> 1; o > 0; o >>= 1) all += __shfl_xor_sync(team.mask, all, o);
+      for (int o = reduce >> 1; o > 0; o >>= 1) all += __shfl_xor_sync(team.mask, all, o);
       s = all > 0.0 ? s / all : 0.0;
     }
-    if (slot) {
-      idx_out[t * r.k + team.rank] = mine;
-      w_out[t * r.k + team.rank] = (float)(s * (double)r.scale);
+    if (chosen) {
+      idx_out[t * r.k + slot] = mine;
+      w_out[t * r.k + slot] = (float)(s * (double)r.scale);
     }
   }
 }
@@ -847,22 +966,24 @@ cudaError_t with(F f) {
   return f(std::integral_constant<int, L>(), std::integral_constant<int, V>());
 }
 
-// Routing: a lane per slot, and one per group at least.
+// Routing: a lane per slot, and one per group at least; up to 8 slots by the merge.
 template <typename F>
 cudaError_t by_choice(const Routing& r, F f) {
+  const auto few = [&](auto l, auto v) { return f(l, v, std::true_type()); };
+  const auto many = [&](auto l, auto v) { return f(l, v, std::false_type()); };
   if (r.k <= 8 && r.groups <= 8) {
-    if (r.E <= 8) return with<8, 1>(f);
-    if (r.E <= 16) return with<8, 2>(f);
-    if (r.E <= 32) return with<8, 4>(f);
-    if (r.E <= 64) return with<8, 8>(f);
-    if (r.E <= 128) return with<8, 16>(f);
-    if (r.E <= 256) return with<16, 16>(f);
-  } else {
-    if (r.E <= 64) return with<32, 2>(f);
-    if (r.E <= 128) return with<32, 4>(f);
-    if (r.E <= 256) return with<32, 8>(f);
+    if (r.E <= 8) return with<8, 1>(few);
+    if (r.E <= 16) return with<8, 2>(few);
+    if (r.E <= 32) return with<8, 4>(few);
+    if (r.E <= 64) return with<8, 8>(few);
+    if (r.E <= 128) return with<8, 16>(few);
+    if (r.E <= 256) return with<16, 16>(few);
+    return with<32, 16>(few);
   }
-  return with<32, 16>(f);
+  if (r.E <= 64) return with<32, 2>(many);
+  if (r.E <= 128) return with<32, 4>(many);
+  if (r.E <= 256) return with<32, 8>(many);
+  return with<32, 16>(many);
 }
 
 // Losses and gradient: a lane per slot.
@@ -894,16 +1015,17 @@ int vectors(const Routing& r, const T* p, int64_t stride) {
 
 cudaError_t launch_route(const Routing& r, const void* logits, const float* bias, int32_t* idx,
                          float* w, cudaStream_t st) {
-  return by_choice(r, [&](auto l, auto v) {
+  return by_choice(r, [&](auto l, auto v, auto few) {
     constexpr int L = decltype(l)::value, V = decltype(v)::value;
+    constexpr bool FEW = decltype(few)::value;
     const dim3 grid(token_blocks<L>(r, V <= 8 ? 3 : 2)), block(32 * kWarps);
     if (r.bf16) {
       const auto* p = static_cast<const __nv_bfloat16*>(logits);
-      return launch_pdl(k_route<__nv_bfloat16, L, V>, grid, block, 0, st, r, p, bias,
+      return launch_pdl(k_route<__nv_bfloat16, L, V, FEW>, grid, block, 0, st, r, p, bias,
                         vectors<__nv_bfloat16, V>(r, p, r.stride), idx, w);
     }
     const auto* p = static_cast<const float*>(logits);
-    return launch_pdl(k_route<float, L, V>, grid, block, 0, st, r, p, bias,
+    return launch_pdl(k_route<float, L, V, FEW>, grid, block, 0, st, r, p, bias,
                       vectors<float, V>(r, p, r.stride), idx, w);
   });
 }
