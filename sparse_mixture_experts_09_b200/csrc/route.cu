@@ -210,7 +210,7 @@ struct Groups {
 };
 
 // The groups that stay, as a ballot (bit base + g * lanes for group g). With CHECK a value may
-// be off by tol + 8 u |value|; `close` is set where the last group that stays and the first
+// be off by tol + 2 u |value|; `close` is set where the last group that stays and the first
 // that goes are not further apart than that allows.
 // A group's one or two best: its lanes take their own values, or every lanes-th from shared
 // memory, and merge their pairs; group_top > 2 takes the largest left group_top times.
@@ -283,7 +283,7 @@ __device__ __forceinline__ unsigned open_groups(const Routing& r, const Team<L>&
   const bool in = above < r.topk_groups;
   if (CHECK) {
     const bool real = g < r.groups;
-    const K off = real ? 2 * tol + (K)0x1p-20 * (fabs(m1) + (r.group_top == 2 ? fabs(m2) : (K)0)) : (K)0;
+    const K off = real ? 2 * tol + (K)0x1p-22 * (fabs(m1) + (r.group_top == 2 ? fabs(m2) : (K)0)) : (K)0;
     const K least = -team.max(real && in ? -mine : none), most = team.max(real && !in ? mine : none);
     close = r.topk_groups < r.groups && !(least - most > 2 * team.max(off));
   }
@@ -294,7 +294,7 @@ __device__ __forceinline__ unsigned open_groups(const Routing& r, const Team<L>&
 // the expert of lane `rank` below n. Each lane sorts its own and lays them out in shared memory;
 // then the team finds the largest head, and the lowest lane that has it gives it up; which
 // expert it was is looked up for all at the end. n = k where the order is exact (tol < 0). Else an
-// order may be off by tol + 8 u |order|: n is the first place from k on at which all that
+// order may be off by tol + 2 u |order|: n is the first place from k on at which all that
 // follow are certainly less, and `close` is set where neighbours among the n may stand in
 // the wrong order. n = 0: not to be had this way (fewer than k finite values, or a run of
 // near ties longer than the team).
@@ -319,7 +319,7 @@ __device__ __forceinline__ int best_experts(const Routing& r, const Team<L>& tea
       break;
     }
     if (tol >= 0.f && j > 0) {
-      const bool far = last_key - m > reach + 0x1p-20f * fabsf(last_key);
+      const bool far = last_key - m > reach + 0x1p-22f * fabsf(last_key);
       if (j >= r.k && far) break;
       if (!far) close = true;
       if (j == L) {
@@ -357,10 +357,10 @@ __device__ __forceinline__ int best_experts(const Routing& r, const Team<L>& tea
 // choice is not to be had this way.
 template <int L, int V>
 __device__ __forceinline__ int best_few(const Routing& r, const Team<L>& team, const float (&order)[V],
-                                        float tol, float2* shared, float& value, int& n, int& slot,
-                                        bool& close, bool& unsure) {
+                                        float tol, float2* shared, int& n, int& slot, bool& close,
+                                        bool& unsure) {
   int mine = team.rank;
-  value = order[0];
+  float value = order[0];
   n = L;
   if constexpr (V > 1) {
     float sorted[V], top[8];
@@ -393,7 +393,7 @@ __device__ __forceinline__ int best_few(const Routing& r, const Team<L>& team, c
       unsure = true;
       return 0;
     }
-    const float low = tol < 0.f ? last : last - (2.f * tol + 0x1p-20f * fabsf(last));
+    const float low = tol < 0.f ? last : last - (2.f * tol + 0x1p-22f * fabsf(last));
     int count = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) count += order[v] >= low;
@@ -422,14 +422,23 @@ __device__ __forceinline__ int best_few(const Routing& r, const Team<L>& team, c
     }
   }
   slot = 0;
-  bool near = false;
-  const float reach = 2.f * tol + 0x1p-20f * fabsf(value);
-  for (int j = 0; j < n; ++j) {
-    const float other = team.from(value, j);
-    slot += other > value || (other == value && j < team.rank);
-    near |= j != team.rank && !(fabsf(other - value) > reach);
+  if (tol < 0.f) {
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      if (V > 1 && j >= n) break;
+      const float other = team.from(value, j);
+      slot += other > value || (other == value && j < team.rank);
+    }
+  } else {
+    bool near = false;
+    const float reach = 2.f * tol + 0x1p-22f * fabsf(value);
+    for (int j = 0; j < n; ++j) {
+      const float other = team.from(value, j);
+      slot += other > value || (other == value && j < team.rank);
+      near |= j != team.rank && !(fabsf(other - value) > reach);
+    }
+    close = __any_sync(team.mask, near && slot < r.k);
   }
-  close = tol >= 0.f && __any_sync(team.mask, near && slot < r.k);
   if (V == 1) unsure = __any_sync(team.mask, slot < r.k && value == -INFINITY);
   return mine;
 }
@@ -475,13 +484,11 @@ __device__ __forceinline__ double sum_in_double(const Team<L>& team, const float
   return team.sum(total);
 }
 
-// The choice with all values in double. Apart from the kernel, whose registers it would
-// crowd.
+// All values of a token in double: s + bias, and with no bias the logits where a group is
+// judged by one expert.
 template <typename T, int L, int V>
-__device__ __noinline__ int choose_in_double(const Routing r, const T* row, const float* bias,
-                                             double* shared) {
-  const Team<L> team;
-  const Groups<L, V> groups(r, team);
+__device__ __forceinline__ void values_in_double(const Routing& r, const Team<L>& team, const T* row,
+                                                 const float* bias, double (&value)[V]) {
   float l[V];
   load_logits<T, V>(row, team.rank, r.E, false, l);
   float mx = -INFINITY;
@@ -489,7 +496,6 @@ __device__ __noinline__ int choose_in_double(const Routing r, const T* row, cons
   for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
   mx = team.max(mx);
   const double total = r.sigmoid ? 1.0 : sum_in_double(team, l, mx);
-  double value[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = team.rank * V + v;
@@ -503,10 +509,31 @@ __device__ __noinline__ int choose_in_double(const Routing r, const T* row, cons
       value[v] = l[v];
     }
   }
+}
+
+// The groups that stay, decided in double; and the whole choice: the expert of lane `rank` < k.
+// Apart from the kernel, whose registers they would crowd.
+template <typename T, int L, int V>
+__device__ __noinline__ unsigned groups_in_double(const Routing r, const T* row, const float* bias,
+                                                  double* shared) {
+  const Team<L> team;
+  const Groups<L, V> groups(r, team);
+  double value[V];
+  values_in_double<T, L, V>(r, team, row, bias, value);
   bool close = false;
-  unsigned stay = 0xffffffffu;
-  if (r.groups > 1) stay = open_groups<false>(r, team, groups, value, 0.0, shared, close);
-  if (!bias) {
+  return open_groups<false>(r, team, groups, value, 0.0, shared, close);
+}
+template <typename T, int L, int V>
+__device__ __noinline__ int choose_in_double(const Routing r, const T* row, const float* bias,
+                                             unsigned stay) {
+  const Team<L> team;
+  const Groups<L, V> groups(r, team);
+  double value[V];
+  if (bias) {
+    values_in_double<T, L, V>(r, team, row, bias, value);
+  } else {
+    float l[V];
+    load_logits<T, V>(row, team.rank, r.E, false, l);
 #pragma unroll
     for (int v = 0; v < V; ++v) value[v] = l[v];
   }
@@ -554,14 +581,14 @@ __device__ __noinline__ int reorder_in_double(const Routing r, const T* row, con
 // candidates from their own values (one a lane), the groups, long rows of ties and rows
 // with fewer than k finite values from all values. Bounds, with u = 2^-24: the exponential is
 // off by 4 u and by 1.5 u |x| for its argument, the reciprocal by 2 u; s (1 - s) is at most
-// 1/4 and |x| s (1 - s) at most 0.23, so a sigmoid is off by less than 5 u (8 u are allowed); |x| e^x
+// 1/4 and |x| s (1 - s) at most 0.23, so a sigmoid is off by less than 5 u (6 u are allowed); |x| e^x
 // is at most 0.37 below 0, so a softmax is off by less than 32 u of the largest probability (its
 // sum of up to 512 terms is a tree of 20 levels); the sum with the bias by u of its value.
 //
 // Bound by instructions, not bytes: a team is as narrow as 16 values per lane allow, so that
 // a warp's instruction serves up to four tokens.
 template <typename T, int L, int V, bool FEW>
-__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
+__global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
     k_route(const Routing r, const T* __restrict__ logits, const float* __restrict__ bias, int vec,
             int32_t* __restrict__ idx_out, float* __restrict__ w_out) {
   pdl_trigger();
@@ -600,7 +627,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
       if (r.sigmoid) {
 #pragma unroll
         for (int v = 0; v < V; ++v) c[v] = fast_rcp(1.f + fast_exp2(-kLog2e * l[v]));
-        tol = 0x1p-21f;
+        tol = 0x1.8p-22f;
       } else {
         float sum = 0.f;
 #pragma unroll
@@ -619,41 +646,42 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
         for (int v = 0; v < V; ++v) c[v] += s_bias[team.rank * V + v];
       }
     }
-    bool close = r.group_top > 2;
-    int mine = 0, n = 0, slot = team.rank;
     unsigned stay = 0xffffffffu;
-    if (r.groups > 1 && !close) {
-      bool near = false;
-      stay = open_groups<true>(r, team, groups, c, tol, reinterpret_cast<float*>(shared), near);
-      close = scores && near;
-    }
-    if (!close) {
-      if (bias) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) l[v] = c[v];
+    if (r.groups > 1) {
+      bool near = r.group_top > 2;
+      if (!near) {
+        stay = open_groups<true>(r, team, groups, c, tol, reinterpret_cast<float*>(shared), near);
+        near = scores && near;
       }
-      if (r.groups > 1) {
-        if (groups.size == V * groups.lanes) {  // one group's all
-          const bool open = groups.stays(stay, 0);
-#pragma unroll
-          for (int v = 0; v < V; ++v) l[v] = open ? l[v] : -INFINITY;
-        } else {
-#pragma unroll
-          for (int v = 0; v < V; ++v) l[v] = groups.stays(stay, v) ? l[v] : -INFINITY;
-        }
-      }
-      bool near = false;
-      float value;
-      if constexpr (FEW)
-        mine = best_few(r, team, l, bias ? tol : -1.f, reinterpret_cast<float2*>(shared), value, n, slot, near, close);
-      else
-        mine = best_experts(r, team, l, bias ? tol : -1.f, reinterpret_cast<float*>(shared), n, near);
-      if (!FEW) close = n == 0;
-      if (near && !close) slot = reorder_in_double<T, L, V>(r, row, bias, mine, n);
+      if (near) stay = groups_in_double<T, L, V>(r, row, bias, shared);
     }
-    if (close) {
-      mine = choose_in_double<T, L, V>(r, row, bias, shared);
+    if (bias) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) l[v] = c[v];
+    }
+    if (r.groups > 1) {
+      if (groups.size == V * groups.lanes) {  // one group's all
+        const bool open = groups.stays(stay, 0);
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = open ? l[v] : -INFINITY;
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = groups.stays(stay, v) ? l[v] : -INFINITY;
+      }
+    }
+    int mine, n = 0, slot = team.rank;
+    bool near = false, unsure = false;
+    if constexpr (FEW) {
+      mine = best_few(r, team, l, bias ? tol : -1.f, reinterpret_cast<float2*>(shared), n, slot, near, unsure);
+    } else {
+      mine = best_experts(r, team, l, bias ? tol : -1.f, reinterpret_cast<float*>(shared), n, near);
+      unsure = n == 0;
+    }
+    if (unsure) {
+      mine = choose_in_double<T, L, V>(r, row, bias, stay);
       slot = team.rank;
+    } else if (near) {
+      slot = reorder_in_double<T, L, V>(r, row, bias, mine, n);
     }
     // weights: one lane per slot, in double, rounded once
     const bool chosen = slot < r.k;
@@ -1018,7 +1046,7 @@ cudaError_t launch_route(const Routing& r, const void* logits, const float* bias
   return by_choice(r, [&](auto l, auto v, auto few) {
     constexpr int L = decltype(l)::value, V = decltype(v)::value;
     constexpr bool FEW = decltype(few)::value;
-    const dim3 grid(token_blocks<L>(r, V <= 8 ? 3 : 2)), block(32 * kWarps);
+    const dim3 grid(token_blocks<L>(r, V <= 4 ? 4 : V <= 8 ? 3 : 2)), block(32 * kWarps);
     if (r.bf16) {
       const auto* p = static_cast<const __nv_bfloat16*>(logits);
       return launch_pdl(k_route<__nv_bfloat16, L, V, FEW>, grid, block, 0, st, r, p, bias,
