@@ -557,7 +557,8 @@ moe_status_t moe_combine_backward(const moe_bf16_t* d_out, const float* y_perm,
  *   8 in [8, 128]; 1 <= num_adapters <= 16384; the strides (elements from one row to the next)
  *   multiples of 8, at least the row's length; x, a, b, base and out 16-byte aligned.
  *   ws: a device workspace of moe_lora_workspace() bytes (256-byte aligned; its content
- *   does not matter). */
+ *   does not matter). moe_lora_workspace() is 0 where none is needed (few rows; ws may then
+ *   be NULL) and where the arguments are invalid (moe_last_error() then says why). */
 typedef struct {
   int64_t num_rows;
   int64_t x_stride;

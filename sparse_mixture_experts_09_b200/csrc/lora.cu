@@ -32,81 +32,84 @@ __device__ __forceinline__ int adapter_of(const Lora& l, int64_t r) {
   return g >= 0 && g < l.G ? g : -1;
 }
 
-// t[r][j] = scale_g <x[r], a_g[j]> for J neighbouring j: one block per (row, J ranks), its
-// threads along the features.
-template <int J>
-__global__ void __launch_bounds__(kThreads) k_shrink_rows(const Lora l, float* __restrict__ t) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ float s_sum[J][kThreads / 32];
-  const int per_row = l.rank / J;
-  const int64_t r = blockIdx.x / per_row;
-  const int j0 = (int)(blockIdx.x - r * per_row) * J;
-  const int g = adapter_of(l, r);
-  if (g < 0) return;
-  const uint4* x = reinterpret_cast<const uint4*>(l.x + r * l.x_stride);
-  const uint4* a = reinterpret_cast<const uint4*>(l.a + ((int64_t)g * l.rank + j0) * l.H);
-  const int vecs = l.H >> 3;
-  float sum[J];
-#pragma unroll
-  for (int j = 0; j < J; ++j) sum[j] = 0.f;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < vecs; i += kThreads) {
-    const uint4 xv = __ldg(x + i);
-#pragma unroll
-    for (int j = 0; j < J; ++j) sum[j] = dot8(xv, __ldg(a + (int64_t)j * vecs + i), sum[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < J; ++j) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
-    if ((threadIdx.x & 31) == 0) s_sum[j][threadIdx.x >> 5] = sum[j];
-  }
-  __syncthreads();
-  if (threadIdx.x < J) {
-    float all = 0.f;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) all += s_sum[threadIdx.x][w];
-    t[r * l.rank + j0 + threadIdx.x] = all * (l.scale ? l.scale[g] : 1.f);
-  }
+// ---- few rows: one cluster of 8 blocks per row, one launch ----
+
+constexpr int kCluster = 8;
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
 }
 
-template <typename T>
-__device__ __forceinline__ float load_out(const T* p) {
-  return (float)*p;
-}
+__device__ __forceinline__ float load_out(float v) { return v; }
+__device__ __forceinline__ float load_out(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// out[r][n] = base[r][n] + <t[r], b_g[n]>. P lanes share an output column (P the power of two
-// from rank / 8 up), each 8 ranks of it in one 16-byte load; a warp takes 32 columns at a
-// time, P of them per lane group, and adds with a butterfly that leaves one column in
-// every lane.
+// Block c of a row's cluster takes the c-th eighth of the features for all ranks (a warp
+// per rank), leaves its sums in every block's shared memory, and after the cluster's barrier
+// each block adds the eighths in order and takes every eighth run of 256 columns. Both
+// products stream the row's adapter once; a second launch, its gap and a workspace between them
+// would cost more than the work of few rows. The first columns' b and base are
+// loaded before the barrier.
+//
+// Columns: P lanes share one (P the power of two from rank / 8 up), each 8 ranks of it in one
+// 16-byte load; a warp takes 32 columns at a time, P of them per lane group, and adds with a
+// butterfly that leaves one column in every lane.
 template <typename T, int P>
-__global__ void __launch_bounds__(kThreads) k_expand_rows(const Lora l, const float* __restrict__ t,
-                                                          int blocks_per_row) {
+__global__ void __launch_bounds__(kThreads) k_lora_rows(const Lora l) {
   pdl_trigger();
   pdl_wait();
-  const int64_t r = blockIdx.x / blocks_per_row;
-  const int first = (int)(blockIdx.x - r * blocks_per_row) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int part = lane % P, col = lane / P;
+  __shared__ float s_part[kCluster][128];
+  constexpr int kWarps = kThreads / 32;
+  const int64_t r = blockIdx.x / kCluster;
+  const int c = (int)(blockIdx.x % kCluster);  // the block's rank in its cluster
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const T* base = static_cast<const T*>(l.base) + r * l.base_stride;
   T* out = static_cast<T*>(l.out) + r * l.out_stride;
+  const int step = kCluster * kWarps * 32;
+  int n0 = (c * kWarps + warp) * 32;
   const int g = adapter_of(l, r);
-  const int step = blocks_per_row * (kThreads / 32) * 32;
-  if (g < 0) {
-    if (static_cast<const void*>(base) != static_cast<const void*>(out))
-      for (int n = first * 32 + lane; n < l.N; n += step) out[n] = base[n];
+  if (g < 0) {  // the whole cluster
+    if (l.base != l.out)
+      for (int n = n0 + lane; n < l.N; n += step) out[n] = base[n];
     return;
   }
-  const bool in = part * 8 < l.rank;
-  float tv[8];
+  // every block of the cluster runs before any writes to its shared memory
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int vecs = l.H >> 3, per = (vecs + kCluster - 1) / kCluster;
+  const int v0 = c * per, v1 = v0 + per < vecs ? v0 + per : vecs;
+  const uint4* x = reinterpret_cast<const uint4*>(l.x + r * l.x_stride);
+  const uint4* a = reinterpret_cast<const uint4*>(l.a + (int64_t)g * l.rank * l.H);
+  float sums[128 / kWarps];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) tv[q] = in ? t[r * l.rank + part * 8 + q] : 0.f;
-  const __nv_bfloat16* b0 = reinterpret_cast<const __nv_bfloat16*>(l.b) + (int64_t)g * l.N * l.rank;
-  for (int n0 = first * 32; n0 < l.N; n0 += step) {
-    uint4 bv[P];
+  for (int q = 0; q < 128 / kWarps; q += 2) {
+    const int j = warp + q * kWarps;
+    sums[q] = sums[q + 1] = 0.f;
+    if (j < l.rank) {  // rank is a multiple of 8: the pair's second is j + 8
+      const bool two = j + kWarps < l.rank;
+      const uint4* a0 = a + (int64_t)j * vecs;
+      const uint4* a1 = two ? a0 + (int64_t)kWarps * vecs : a0;
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+      for (int i = v0 + lane; i < v1; i += 32) {
+        const uint4 xv = __ldg(x + i), q0 = __ldg(a0 + i), q1 = __ldg(a1 + i);
+        s0 = dot8(xv, q0, s0);
+        s1 = dot8(xv, q1, s1);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+        s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+      }
+      sums[q] = s0;
+      sums[q + 1] = s1;
+    }
+  }
+  const int part = lane % P, col = lane / P;
+  const bool in = part * 8 < l.rank;
+  const uint16_t* b0 = l.b + (int64_t)g * l.N * l.rank;
+  uint4 bv[P];
+  const auto load_b = [&](int n0) {
 #pragma unroll
     for (int u = 0; u < P; ++u) {
       const int n = n0 + u * (32 / P) + col;
@@ -114,8 +117,34 @@ __global__ void __launch_bounds__(kThreads) k_expand_rows(const Lora l, const fl
       if (in && n < l.N)
         bv[u] = __ldg(reinterpret_cast<const uint4*>(b0 + (int64_t)n * l.rank + part * 8));
     }
-    const int mine = n0 + part * (32 / P) + col;
-    const float was = mine < l.N ? load_out(base + mine) : 0.f;
+  };
+  load_b(n0);
+  int mine = n0 + part * (32 / P) + col;
+  float was = mine < l.N ? load_out(base[mine]) : 0.f;
+  const float scale = l.scale ? l.scale[g] : 1.f;
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // lane q < 8 hands the warp's sums to block q
+  if (lane < kCluster) {
+    uint32_t there;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(smem_addr(&s_part[c][warp])), "r"(lane));
+#pragma unroll
+    for (int q = 0; q < 128 / kWarps; ++q)
+      if (warp + q * kWarps < l.rank)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there + q * kWarps * 4), "f"(sums[q]) : "memory");
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  float tv[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    float s = 0.f;
+    if (in) {
+#pragma unroll
+      for (int w = 0; w < kCluster; ++w) s += s_part[w][part * 8 + q];
+    }
+    tv[q] = s * scale;
+  }
+  while (n0 < l.N) {
     float sum[P];
 #pragma unroll
     for (int u = 0; u < P; ++u) {
@@ -128,6 +157,14 @@ __global__ void __launch_bounds__(kThreads) k_expand_rows(const Lora l, const fl
       }
       sum[u] = s;
     }
+    const float before = was;
+    const int here = mine;
+    n0 += step;
+    if (n0 < l.N) {  // the next columns, while these are added up
+      load_b(n0);
+      mine = n0 + part * (32 / P) + col;
+      was = mine < l.N ? load_out(base[mine]) : 0.f;
+    }
     // lane `part` ends with column u = part: halve the columns held at each step
 #pragma unroll
     for (int o = P / 2; o > 0; o >>= 1) {
@@ -139,19 +176,35 @@ __global__ void __launch_bounds__(kThreads) k_expand_rows(const Lora l, const fl
         sum[u] = keep + __shfl_xor_sync(0xffffffffu, give, o);
       }
     }
-    if (mine < l.N) store_out(out + mine, was + sum[0]);
+    if (here < l.N) store_out(out + here, before + sum[0]);
   }
 }
 
+template <typename T, int P>
+cudaError_t run_rows(const Lora& l, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(l.R * kCluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_lora_rows<T, P>, l);
+}
+
 template <typename T>
-cudaError_t expand_rows(const Lora& l, const float* t, cudaStream_t st) {
-  const int blocks_per_row = (l.N + 32 * (kThreads / 32) - 1) / (32 * (kThreads / 32));
-  const dim3 grid((unsigned)(l.R * blocks_per_row)), block(kThreads);
-  if (l.rank <= 8) return launch_pdl(k_expand_rows<T, 1>, grid, block, 0, st, l, t, blocks_per_row);
-  if (l.rank <= 16) return launch_pdl(k_expand_rows<T, 2>, grid, block, 0, st, l, t, blocks_per_row);
-  if (l.rank <= 32) return launch_pdl(k_expand_rows<T, 4>, grid, block, 0, st, l, t, blocks_per_row);
-  if (l.rank <= 64) return launch_pdl(k_expand_rows<T, 8>, grid, block, 0, st, l, t, blocks_per_row);
-  return launch_pdl(k_expand_rows<T, 16>, grid, block, 0, st, l, t, blocks_per_row);
+cudaError_t few_rows(const Lora& l, cudaStream_t st) {
+  if (l.rank <= 8) return run_rows<T, 1>(l, st);
+  if (l.rank <= 16) return run_rows<T, 2>(l, st);
+  if (l.rank <= 32) return run_rows<T, 4>(l, st);
+  if (l.rank <= 64) return run_rows<T, 8>(l, st);
+  return run_rows<T, 16>(l, st);
 }
 
 // ---- many rows: tiles of up to 64 rows of one adapter on the matrix pipe ----
@@ -254,9 +307,6 @@ __global__ void __launch_bounds__(1024) k_plan(const Lora l, Plan p) {
   }
 }
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
 // 16 bytes from global to shared memory; zeros when !in (nothing is read then).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0)
@@ -617,7 +667,7 @@ cudaError_t run_tiles(const Lora& l, const Plan& p, cudaStream_t st) {
 }  // namespace
 
 size_t lora_workspace(const Lora& l) {
-  if (l.R < kTilesFrom) return up256((size_t)l.R * l.rank * 4) + 256;
+  if (l.R < kTilesFrom) return 0;
   size_t end = 0;
   plan_at(l, nullptr, &end);
   return end;
@@ -639,20 +689,7 @@ cudaError_t launch_lora(const Lora& l, void* ws, cudaStream_t st) {
       default: return run_tiles<128>(l, p, st);
     }
   }
-  float* t = static_cast<float*>(ws);
-  // ranks per block: more blocks for few rows, fewer passes over x for many
-  const int64_t pairs = l.R * l.rank;
-  const int64_t want = (int64_t)num_sms() * 2;
-  const dim3 block(kThreads);
-  cudaError_t e;
-  if (pairs <= want)
-    e = launch_pdl(k_shrink_rows<1>, dim3((unsigned)pairs), block, 0, st, l, t);
-  else if (pairs <= 4 * want)
-    e = launch_pdl(k_shrink_rows<2>, dim3((unsigned)(pairs / 2)), block, 0, st, l, t);
-  else
-    e = launch_pdl(k_shrink_rows<8>, dim3((unsigned)(pairs / 8)), block, 0, st, l, t);
-  if (e != cudaSuccess) return e;
-  return l.fp32 ? expand_rows<float>(l, t, st) : expand_rows<__nv_bfloat16>(l, t, st);
+  return l.fp32 ? few_rows<float>(l, st) : few_rows<__nv_bfloat16>(l, st);
 }
 
 }  // namespace moe

@@ -288,7 +288,7 @@ moe_status_t moe_lora_add(const moe_lora_t* lora, const void* base, const moe_bf
   if (out == base && l.out_stride != l.base_stride)
     return fail_with(MOE_ERR_INVALID_ARG, "out is base, but their strides differ");
   const size_t need = lora_workspace(l);
-  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256)
+  if (need && (!ws || reinterpret_cast<uintptr_t>(ws) % 256))
     return fail_with(MOE_ERR_WORKSPACE, "workspace is NULL or not 256-byte aligned");
   if (ws_bytes < need)
     return fail_with(MOE_ERR_WORKSPACE, "workspace too small: need %zu bytes, got %zu", need, ws_bytes);

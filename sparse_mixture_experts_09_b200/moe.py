@@ -791,22 +791,35 @@ def _on(device: torch.device, stream, call):
         return call(stream.cuda_stream)
 
 
-def _arg(t, name: str, dtypes, shape, device=None) -> Optional[int]:
-    """The address of a contiguous CUDA tensor of one of `dtypes` and of exactly `shape`."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+def _arg(t, name: str, dtypes, shape, device=None) -> int:
+    """The address of a contiguous CUDA tensor of one of `dtypes`, of exactly `shape`, on
+    `device` (None: any)."""
+    if (t.is_cuda and t.shape == shape and t.dtype in dtypes and t.is_contiguous()
+            and (device is None or t.device == device)):
+        return t.data_ptr()
+    return _rows(t, name, dtypes, shape, device, contiguous=True)
+
+
+def _rows(t, name: str, dtypes, shape, device=None, contiguous: bool = False) -> int:
+    """As _arg for a tensor whose rows are contiguous and may be strided (its row stride is
+    a matter for the caller); names what is wrong."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
+    if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its rows")
     return t.data_ptr()
 
 
-_F32, _I32, _LOGITS = (torch.float32,), (torch.int32,), (torch.float32, torch.bfloat16)
+_F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+_LOGITS = (torch.float32, torch.bfloat16)
 
 
 def _routing_args(logits, routing: Routing) -> _RoutingArgs:
@@ -931,21 +944,6 @@ def combine_backward(d_out, y_perm, row_of, topk_w, counts=None, offsets=None, n
 
 # ---- low-rank adapters of many requests beside a shared projection ----
 
-def _rows(t, name: str, dtypes, shape, device=None):
-    """(address, row stride) of a 2-D CUDA tensor whose rows are contiguous."""
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must be contiguous along its rows")
-    return t.data_ptr(), (t.stride(0) if shape[0] > 1 else shape[1])
-
-
 def lora_add(base, x, a, b, adapter, scale=None, out=None, stream=None):
     """base + scale[g] * (x a[g]^T) b[g]^T per row, g = adapter[row] (int32; a value outside
     [0, G) is a row without an adapter): base [R, N] bf16 or fp32, x [R, H] bf16, a [G, rank, H]
@@ -957,20 +955,23 @@ def lora_add(base, x, a, b, adapter, scale=None, out=None, stream=None):
     ad, rank, _ = a.shape
     n = b.shape[1]
     dev = x.device
-    xp, xs = _rows(x, "x", (torch.bfloat16,), (r, h))
-    ap = _arg(a, "a", (torch.bfloat16,), (ad, rank, h), dev)
-    bp = _arg(b, "b", (torch.bfloat16,), (ad, n, rank), dev)
+    xp = _rows(x, "x", _BF16, (r, h))
+    ap = _arg(a, "a", _BF16, (ad, rank, h), dev)
+    bp = _arg(b, "b", _BF16, (ad, n, rank), dev)
     ip = _arg(adapter, "adapter", _I32, (r,), dev)
     sp = None if scale is None else _arg(scale, "scale", _F32, (ad,), dev)
-    base_p, base_s = _rows(base, "base", _LOGITS, (r, n), dev)
+    base_p = _rows(base, "base", _LOGITS, (r, n), dev)
 
     def call(st):
-        dst = torch.empty((r, n), dtype=base.dtype, device=dev) if out is None else out
-        out_p, out_s = _rows(dst, "out", (base.dtype,), (r, n), dev)
-        args = _LoraArgs(r, xs, base_s, out_s, h, n, rank, ad, int(base.dtype == torch.float32))
-        size = lib().moe_lora_workspace(args)
-        ws = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
-        _check(lib().moe_lora_add(args, base_p, xp, ap, bp, ip, sp, out_p, ws.data_ptr(), size, st))
+        dst = torch.empty_strided((r, n), (n, 1), dtype=base.dtype, device=dev) if out is None else out
+        out_p = dst.data_ptr() if out is None else _rows(out, "out", (base.dtype,), (r, n), dev)
+        # one row has no stride to speak of
+        args = _LoraArgs(r, x.stride(0) if r > 1 else h, base.stride(0) if r > 1 else n,
+                         dst.stride(0) if r > 1 else n, h, n, rank, ad, int(base.dtype == torch.float32))
+        size = lib().moe_lora_workspace(args)      # 0: few rows need none
+        ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        _check(lib().moe_lora_add(args, base_p, xp, ap, bp, ip, sp, out_p,
+                                  None if ws is None else ws.data_ptr(), size, st))
         return dst
 
     return _on(dev, stream, call)

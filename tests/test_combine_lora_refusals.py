@@ -56,7 +56,7 @@ def test_lora_sizes_are_refused(L, bad):
                                         (dict(b=None), 1), (dict(b=8), 1), (dict(ids=None), 1), (dict(ids=2), 1), (dict(scale=2), 1),
                                         (dict(out=None), 1), (dict(out=8), 1), (dict(ws=None), 3), (dict(ws=128), 3), (dict(size=0), 3)])
 def test_lora_pointers_are_refused(L, bad, status):
-    assert add(L, lora(), **bad) == status
+    assert add(L, lora(num_rows=1000), **bad) == status
     assert L.moe_last_error()
 
 
@@ -64,7 +64,9 @@ def test_lora_aliases_and_empty(L):
     assert add(L, lora(out_stride=40), base=16, out=16) == 1       # in place with another stride
     assert add(L, None) == 1
     assert add(L, lora(num_rows=0), base=None, x=None, ids=None, out=None, ws=None, size=0) == 0
-    assert L.moe_lora_workspace(lora()) >= 4 * 16 * 4
+    # many rows: the sorted row numbers and the rank-wide sums at least
+    assert L.moe_lora_workspace(lora(num_rows=1000)) >= 1000 * (4 + 16 * 4)
+    assert L.moe_lora_workspace(lora()) == 0 and not L.moe_last_error()   # few rows need none
 
 
 def test_binding_refuses():
