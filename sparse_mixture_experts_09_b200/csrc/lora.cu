@@ -224,6 +224,7 @@ constexpr int kTileRows = 64;
 constexpr int kChunkK = 64;    // features per stage of the shrink
 constexpr int kStages = 4;     // of the shrink
 constexpr int kChunkN = 128;   // columns per step of the expand
+constexpr int kMaxSlices = 8;  // of the features
 
 // In the workspace: the tiles {adapter or -1, first sorted row, rows, 0}, their count, the
 // sorted row numbers, and the shrink's sums [slices][R][RP].
@@ -249,13 +250,24 @@ __global__ void __launch_bounds__(1024) k_plan(const Lora l, Plan p) {
   const int groups = l.G + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int g = threadIdx.x; g < groups; g += 1024) s_cursor[g] = 0;
   __syncthreads();
+  constexpr int kKept = 4;  // rounds whose groups stay in registers
+  int kept[kKept];
+  const auto group_of = [&](int64_t r) {
+    if (r >= l.R) return -1;
+    const int g = l.adapter[r];
+    return g >= 0 && g < l.G ? g : l.G;
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i) kept[i] = group_of(i * 1024 + threadIdx.x);
   const int64_t rounds = (l.R + 1023) / 1024;
-  for (int64_t i = 0; i < rounds; ++i) {
-    const int64_t r = i * 1024 + threadIdx.x;
-    const int g = r < l.R ? (adapter_of(l, r) < 0 ? l.G : l.adapter[r]) : -1;
+  const auto count = [&](int g) {
     const unsigned same = __match_any_sync(0xffffffffu, g);
     if (g >= 0 && lane == __ffs(same) - 1) atomicAdd(&s_cursor[g], __popc(same));
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (i < rounds) count(kept[i]);
+  for (int64_t i = kKept; i < rounds; ++i) count(group_of(i * 1024 + threadIdx.x));
   __syncthreads();
   // exclusive prefixes of rows and tiles over the groups: `per` neighbouring groups a thread
   const int per = (groups + 1023) / 1024;
@@ -296,14 +308,19 @@ __global__ void __launch_bounds__(1024) k_plan(const Lora l, Plan p) {
     row_at += n;
   }
   __syncthreads();
-  for (int64_t i = 0; i < rounds; ++i) {
-    const int64_t r = i * 1024 + threadIdx.x;
-    const int g = r < l.R ? (adapter_of(l, r) < 0 ? l.G : l.adapter[r]) : -1;
+  const auto place = [&](int64_t r, int g) {
     const unsigned same = __match_any_sync(0xffffffffu, g);
     int at = 0;
     if (g >= 0 && lane == __ffs(same) - 1) at = atomicAdd(&s_cursor[g], __popc(same));
     at = __shfl_sync(0xffffffffu, at, __ffs(same) - 1);
     if (g >= 0) p.order[at + __popc(same & ((1u << lane) - 1u))] = (int32_t)r;
+  };
+#pragma unroll
+  for (int i = 0; i < kKept; ++i)
+    if (i < rounds) place(i * 1024 + threadIdx.x, kept[i]);
+  for (int64_t i = kKept; i < rounds; ++i) {
+    const int64_t r = i * 1024 + threadIdx.x;
+    place(r, group_of(r));
   }
 }
 
@@ -496,44 +513,63 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1)
   }
   const uint32_t t_at = smem_addr(smem), b_at = t_at + kParts * kTileRows * kPitch;
   constexpr int kStepBytes = kChunkN * kPitch;
-  const uint16_t* bg = l.b + (int64_t)tl.x * l.N * l.rank;
-  auto load_b = [&](int s) {
-    constexpr int kPieces = RP / 8;
-    const uint32_t st = b_at + (s & 1) * kStepBytes;
+  // this thread's pieces of a step of b: the shared address and the column of each
+  constexpr int kPieces = RP / 8, kMine = kChunkN * kPieces / 256;
+  uint32_t b_dst[kMine];
+  int b_col[kMine];
 #pragma unroll
-    for (int i = 0; i < kChunkN * kPieces / 256; ++i) {
-      const int q = tid + 256 * i, n = q / kPieces, piece = q - n * kPieces;
-      const int col = s * kChunkN + n;
-      const bool in = s < s1 && col < l.N && piece * 8 < l.rank;
-      // column n = 8 kWide G + 2 kWide c + 2 w + e sits at row 8 kWide G + 8 w + 2 c + e
-      const int row = n / (8 * kWide) * (8 * kWide) + (n % (2 * kWide)) / 2 * 8 +
-                      (n % (8 * kWide)) / (2 * kWide) * 2 + (n & 1);
-      copy16(st + row * kPitch + piece * 16, in ? bg + (int64_t)col * l.rank + piece * 8 : l.b, in);
+  for (int i = 0; i < kMine; ++i) {
+    const int q = tid + 256 * i, n = q / kPieces;
+    // column n = 8 kWide G + 2 kWide c + 2 w + e sits at row 8 kWide G + 8 w + 2 c + e
+    const int row = n / (8 * kWide) * (8 * kWide) + (n % (2 * kWide)) / 2 * 8 +
+                    (n % (8 * kWide)) / (2 * kWide) * 2 + (n & 1);
+    b_dst[i] = b_at + row * kPitch + q % kPieces * 16;
+    b_col[i] = n;
+  }
+  const int b_piece = tid % kPieces * 8;
+  const bool b_in = b_piece < l.rank;
+  const uint16_t* bg = l.b + (int64_t)tl.x * l.N * l.rank + b_piece;
+  auto load_b = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int col = s * kChunkN + b_col[i];
+      const bool in = b_in && s < s1 && col < l.N;
+      copy16(b_dst[i] + (s & 1) * kStepBytes, in ? bg + (int64_t)col * l.rank : l.b, in);
     }
     copies_end();
   };
   load_b(s0);
-  // t: the slices in order, the scale, the parts
+  // t: the slices in order, the scale, the parts. All of a thread's loads of four ranks go out
+  // together.
   const float scale = l.scale ? l.scale[tl.x] : 1.f;
-  for (int i = tid; i < kTileRows * RP / 2; i += 256) {
-    const int r = i / (RP / 2), c = (i - r * (RP / 2)) * 2;
-    float2 v = make_float2(0.f, 0.f);
-    if (r < tl.z) {
-      const float* src = p.part + (int64_t)(tl.y + r) * RP + c;
-      for (int s = 0; s < slices; ++s) {
-        const float2 q = *reinterpret_cast<const float2*>(src + (int64_t)s * l.R * RP);
-        v.x += q.x;
-        v.y += q.y;
-      }
-      v.x *= scale;
-      v.y *= scale;
+#pragma unroll 2
+  for (int i = tid; i < kTileRows * RP / 4; i += 256) {
+    const int r = i / (RP / 4), c = (i - r * (RP / 4)) * 4;
+    const float* src = p.part + (int64_t)(tl.y + r) * RP + c;
+    float4 q[kMaxSlices];
+#pragma unroll
+    for (int s = 0; s < kMaxSlices; ++s) {
+      q[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < tl.z && s < slices) q[s] = *reinterpret_cast<const float4*>(src + (int64_t)s * l.R * RP);
+    }
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < kMaxSlices; ++s) {
+      v[0] += q[s].x;
+      v[1] += q[s].y;
+      v[2] += q[s].z;
+      v[3] += q[s].w;
     }
 #pragma unroll
+    for (int n = 0; n < 4; ++n) v[n] *= scale;
+#pragma unroll
     for (int part = 0; part < kParts; ++part) {
-      const uint32_t both = pack2(v.x, v.y);
-      *reinterpret_cast<uint32_t*>(smem + (part * kTileRows + r) * kPitch + c * 2) = both;
-      v.x -= lo(both);
-      v.y -= hi(both);
+      const uint2 both = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+      *reinterpret_cast<uint2*>(smem + (part * kTileRows + r) * kPitch + c * 2) = both;
+      v[0] -= lo(both.x);
+      v[1] -= hi(both.x);
+      v[2] -= lo(both.y);
+      v[3] -= hi(both.y);
     }
   }
   const int wr = (warp & 3) * 16, wc = (warp >> 2) * 64;
@@ -541,20 +577,22 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1)
   const bool in0 = r0 < tl.z, in1 = r1 < tl.z;
   const int64_t g0 = in0 ? p.order[tl.y + r0] : 0, g1 = in1 ? p.order[tl.y + r1] : 0;
   constexpr int kGroups = 64 / (8 * kWide);
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int s = s0; s < s1; ++s) {
+  // base is read a step ahead, into the registers that the step before has just stored
+  const T* from[2] = {base + g0 * l.base_stride, base + g1 * l.base_stride};
+  T* to[2] = {out + g0 * l.out_stride, out + g1 * l.out_stride};
+  const bool in_row[2] = {in0, in1};
+  uint4 was[2][kGroups];
+  int col0 = s0 * kChunkN + wc + (lane & 3) * kVec;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (in_row[h] && col0 + g * 8 * kWide < l.N)
+        was[h][g] = *reinterpret_cast<const uint4*>(from[h] + col0 + g * 8 * kWide);
+  for (int s = s0; s < s1; ++s, col0 += kChunkN) {
     copies_wait<0>();
     __syncthreads();
     load_b(s + 1);
-    uint4 was[2][kGroups];
-    const int col0 = s * kChunkN + wc + (lane & 3) * kVec;
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int col = col0 + g * 8 * kWide;
-      const bool in = col < l.N;
-      was[0][g] = in && in0 ? *reinterpret_cast<const uint4*>(base + g0 * l.base_stride + col) : zero;
-      was[1][g] = in && in1 ? *reinterpret_cast<const uint4*>(base + g1 * l.base_stride + col) : zero;
-    }
     float acc[8][4];
 #pragma unroll
     for (int n = 0; n < 8; ++n)
@@ -579,21 +617,24 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1)
         }
       }
     }
+    const int ahead = s + 1 < s1 ? kChunkN : l.N;
 #pragma unroll
     for (int g = 0; g < kGroups; ++g) {
       const int col = col0 + g * 8 * kWide;
-      if (col >= l.N) continue;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (!(h ? in1 : in0)) continue;
-        float f[kVec];
-        Vec<T>::get(was[h][g], f);
+        if (in_row[h] && col < l.N) {
+          float f[kVec];
+          Vec<T>::get(was[h][g], f);
 #pragma unroll
-        for (int w = 0; w < kWide; ++w) {
-          f[2 * w] += acc[g * kWide + w][2 * h];
-          f[2 * w + 1] += acc[g * kWide + w][2 * h + 1];
+          for (int w = 0; w < kWide; ++w) {
+            f[2 * w] += acc[g * kWide + w][2 * h];
+            f[2 * w + 1] += acc[g * kWide + w][2 * h + 1];
+          }
+          *reinterpret_cast<uint4*>(to[h] + col) = Vec<T>::put(f);
         }
-        *reinterpret_cast<uint4*>(out + (h ? g1 : g0) * l.out_stride + col) = Vec<T>::put(f);
+        if (in_row[h] && col + ahead < l.N)
+          was[h][g] = *reinterpret_cast<const uint4*>(from[h] + col + ahead);
       }
     }
   }
@@ -605,13 +646,17 @@ int rank_pad(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ?
 // Rows from which the tiles are used.
 constexpr int64_t kTilesFrom = 128;
 
-// Slices of the features: enough blocks for four on every SM, at least two stages each.
+// Slices of the features: as many blocks as the SMs hold at once (three each; a second
+// round for a few blocks would double the time), at least two stages each. How many tiles
+// the adapters leave partly filled is not known here; twice the full ones is the most
+// allowed for.
 int feature_slices(const Lora& l) {
-  const int64_t tiles = (l.R + kTileRows - 1) / kTileRows;
+  const int64_t full = (l.R + kTileRows - 1) / kTileRows, most = max_tiles(l.R, l.G);
+  const int64_t tiles = most < 2 * full ? most : 2 * full;
   const int64_t chunks = (l.H + kChunkK - 1) / kChunkK;
-  int64_t s = ((int64_t)num_sms() * 4 + tiles - 1) / tiles;
+  int64_t s = (int64_t)num_sms() * 3 / tiles;
   if (s > chunks / 2) s = chunks / 2;
-  return s < 1 ? 1 : s > 8 ? 8 : (int)s;
+  return s < 1 ? 1 : s > kMaxSlices ? kMaxSlices : (int)s;
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }

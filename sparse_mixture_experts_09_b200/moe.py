@@ -754,8 +754,7 @@ def combine_peer(y_bases, y_rows: int, slot_rank, slot_row, topk_w, hidden: int,
 _SCORING = {"softmax": 0, "sigmoid": 1}
 
 
-@dataclass(frozen=True)
-class Routing:
+class Routing(NamedTuple):
     """A routing rule (include/moe.h): k experts per token by softmax or sigmoid scores;
     with num_groups > 1 only the topk_groups groups whose group_top best experts sum
     highest are open; the weights are renormalised to sum to 1 (or not), times scale."""
@@ -850,8 +849,8 @@ def route(logits, routing: Routing, bias=None, stream=None):
     b = None if bias is None else _arg(bias, "bias", _F32, (e,), dev)
 
     def call(st):
-        idx = torch.empty((t, routing.k), dtype=torch.int32, device=dev)
-        w = torch.empty((t, routing.k), dtype=torch.float32, device=dev)
+        idx = torch.empty(t, routing.k, dtype=torch.int32, device=dev)
+        w = torch.empty(t, routing.k, dtype=torch.float32, device=dev)
         _check(lib().moe_route(args, logits.data_ptr(), b, idx.data_ptr(), w.data_ptr(), st))
         return idx, w
 
@@ -901,7 +900,7 @@ def route_backward(logits, topk_idx, routing: Routing, d_topk_w=None, counts=Non
     mask = _token_mask(token_mask, t, dev)
 
     def call(st):
-        out = torch.empty((t, e), dtype=logits.dtype, device=dev)
+        out = torch.empty(t, e, dtype=logits.dtype, device=dev)
         _check(lib().moe_route_backward(args, logits.data_ptr(), idx, dw, c, dl, mask,
                                         out.data_ptr(), st))
         return out
@@ -933,8 +932,8 @@ def combine_backward(d_out, y_perm, row_of, topk_w, counts=None, offsets=None, n
         o = _arg(offsets, "offsets", _I32, (e + 1,), dev)
 
     def call(st):
-        dy = torch.empty((rows, h), dtype=torch.float32, device=dev) if need_dy else None
-        dw = torch.empty((t, k), dtype=torch.float32, device=dev) if need_dw else None
+        dy = torch.empty(rows, h, dtype=torch.float32, device=dev) if need_dy else None
+        dw = torch.empty(t, k, dtype=torch.float32, device=dev) if need_dw else None
         _check(lib().moe_combine_backward(d, y, r, w, c, o, dy.data_ptr() if need_dy else None,
                                           dw.data_ptr() if need_dw else None, t, k, h, e, rows, st))
         return dy, dw
@@ -963,7 +962,7 @@ def lora_add(base, x, a, b, adapter, scale=None, out=None, stream=None):
     base_p = _rows(base, "base", _LOGITS, (r, n), dev)
 
     def call(st):
-        dst = torch.empty_strided((r, n), (n, 1), dtype=base.dtype, device=dev) if out is None else out
+        dst = torch.empty(r, n, dtype=base.dtype, device=dev) if out is None else out
         out_p = dst.data_ptr() if out is None else _rows(out, "out", (base.dtype,), (r, n), dev)
         # one row has no stride to speak of
         args = _LoraArgs(r, x.stride(0) if r > 1 else h, base.stride(0) if r > 1 else n,
