@@ -15,6 +15,12 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ float lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
 __device__ __forceinline__ float dot8(uint4 a, uint4 b, float s) {
   s = fmaf(lo(a.x), lo(b.x), s);
   s = fmaf(hi(a.x), hi(b.x), s);
@@ -38,6 +44,11 @@ constexpr int kCluster = 8;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ float load_out(float v) { return v; }
@@ -132,8 +143,7 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows(const Lora l) {
       if (warp + q * kWarps < l.rank)
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(there + q * kWarps * 4), "f"(sums[q]) : "memory");
   }
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  cluster_sync();
   float tv[8];
 #pragma unroll
   for (int q = 0; q < 8; ++q) {
@@ -180,22 +190,30 @@ __global__ void __launch_bounds__(kThreads) k_lora_rows(const Lora l) {
   }
 }
 
-template <typename T, int P>
-cudaError_t run_rows(const Lora& l, cudaStream_t st) {
+// launch_pdl with a cluster of `cluster` neighbouring blocks.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem,
+                           unsigned cluster, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(l.R * kCluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_lora_rows<T, P>, l);
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+template <typename T, int P>
+cudaError_t run_rows(const Lora& l, cudaStream_t st) {
+  return launch_cluster(k_lora_rows<T, P>, (unsigned)(l.R * kCluster), kThreads, 0, kCluster, st, l);
 }
 
 template <typename T>
@@ -223,16 +241,17 @@ cudaError_t few_rows(const Lora& l, cudaStream_t st) {
 constexpr int kTileRows = 64;
 constexpr int kChunkK = 64;    // features per stage of the shrink
 constexpr int kStages = 4;     // of the shrink
-constexpr int kChunkN = 128;   // columns per step of the expand
+constexpr int kChunkN = 64;    // columns per step of the expand
+constexpr int kAhead = 2;      // steps of the expand in flight
 constexpr int kMaxSlices = 8;  // of the features
 
 // In the workspace: the tiles {adapter or -1, first sorted row, rows, 0}, their count, the
-// sorted row numbers, and the shrink's sums [slices][R][RP].
+// sorted row numbers, and t = scale x a^T of each tile in bf16 parts [tile][part][64][RP].
 struct Plan {
   int4* tiles;
   int32_t* count;
   int32_t* order;
-  float* part;
+  uint16_t* t;
 };
 
 __host__ __device__ inline int64_t max_tiles(int64_t R, int G) {
@@ -350,7 +369,9 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 // to 16, 32, 64 or 128). x and a come in stages of 64 features by 16-byte asynchronous
 // copies, their 16-byte pieces swizzled by the row. The matrix pipe's own sums are
 // truncated, not rounded, at each step, so they run over one stage only (4 steps) and are
-// added to the running sums by ordinary additions.
+// added to the running sums by ordinary additions. The slices of a tile are a cluster: its
+// blocks add them up through distributed shared memory and cut t = scale x a^T into bf16 parts whose sum holds it to 2^-24 (3 parts, fp32 out) or
+// 2^-16 (2 parts, bf16 out: far below its one rounding).
 template <int RP>
 __global__ void __launch_bounds__(128) k_shrink_tiles(const Lora l, const Plan p, int slices) {
   pdl_trigger();
@@ -432,15 +453,47 @@ __global__ void __launch_bounds__(128) k_shrink_tiles(const Lora l, const Plan p
       for (int i = 0; i < 4; ++i) sum[n][i] += acc[n][i];
   }
   copies_wait<0>();
-  float* out = p.part + (int64_t)slice * l.R * RP;
+  // the slices, in their order: each block of the cluster adds up a share of the tile
+  __syncthreads();
+  float* mine = reinterpret_cast<float*>(smem);  // [64][RP]
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = warp * 16 + (lane >> 2) + 8 * h;
-    if (r >= tl.z) continue;
-    float2* o = reinterpret_cast<float2*>(out + (int64_t)(tl.y + r) * RP + (lane & 3) * 2);
+    float2* o = reinterpret_cast<float2*>(mine + r * RP + (lane & 3) * 2);
 #pragma unroll
     for (int n = 0; n < RP / 8; ++n) o[n * 4] = make_float2(sum[n][2 * h], sum[n][2 * h + 1]);
   }
+  cluster_sync();
+  const float scale = l.scale ? l.scale[tl.x] : 1.f;
+  const int parts = l.fp32 ? 3 : 2;
+  for (int i = slice * 128 + tid; i < kTileRows * RP / 4; i += 128 * slices) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < kMaxSlices; ++s) {
+      if (s >= slices) break;
+      uint32_t at;
+      float4 q;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(base + i * 16), "r"(s));
+      asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                   : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w) : "r"(at) : "memory");
+      v[0] += q.x;
+      v[1] += q.y;
+      v[2] += q.z;
+      v[3] += q.w;
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) v[n] *= scale;
+    uint16_t* t = p.t + (int64_t)tile * parts * kTileRows * RP + i * 4;
+    for (int part = 0; part < parts; ++part) {
+      const uint2 both = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+      *reinterpret_cast<uint2*>(t + part * kTileRows * RP) = both;
+      v[0] -= lo(both.x);
+      v[1] -= hi(both.x);
+      v[2] -= lo(both.y);
+      v[3] -= hi(both.y);
+    }
+  }
+  cluster_sync();  // no block leaves while another reads its sums
 }
 
 // Sixteen bytes of the output in floats, and back (one rounding for bf16).
@@ -458,11 +511,6 @@ struct Vec<float> {
                       __float_as_uint(f[3]));
   }
 };
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kN = 8;
@@ -475,15 +523,15 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// One tile and a run of columns, 128 columns a step: 8 warps as 4 (16 rows) x 2 (64 columns).
-// t (the slices' sum, times the scale) is cut into bf16 parts whose sum holds it to 2^-24
-// (3 parts, fp32 out) or 2^-16 (2 parts, bf16 out: far below its one rounding), so the
-// products with b are exact in fp32. b's rows of a step go to shared memory in the order
-// in which a thread's columns of neighbouring 8-wide products are neighbours in out:
-// base is read and out is written 16 bytes at a time straight from the registers.
+// out = base + t b^T. The tiles' steps of 64 columns, in a row, are cut evenly among as many
+// blocks as run at once; a block takes its steps tile by tile. 8 warps as 4 (16 rows) x 2 (32
+// columns). t's parts times b are exact in fp32; t's fragments stay in registers up to rank 64.
+// base and b come by 16-byte asynchronous copies two steps ahead: what has to be in flight
+// to keep HBM busy (some 50 KB an SM) would not fit the registers beside the sums. b's rows
+// go to shared memory in the order in which a thread's columns of neighbouring 8-wide
+// products are neighbours in out, so that out is written 16 bytes at a time.
 template <typename T, int RP>
-__global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1)
-    k_expand_tiles(const Lora l, const Plan p, int slices, int col_runs, int steps_per_run) {
+__global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lora l, const Plan p) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(128) uint8_t smem[];
@@ -491,154 +539,161 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1)
   constexpr int kPitch = RP * 2 + 16;  // odd in 16-byte units: ldmatrix rows fall on distinct banks
   constexpr int kVec = Vec<T>::kN;     // columns of one 16-byte access
   constexpr int kWide = kVec / 2;      // 8-wide products that share it
-  const int tile = blockIdx.x / col_runs, run = blockIdx.x - tile * col_runs;
-  if (tile >= *p.count) return;
-  const int4 tl = p.tiles[tile];
+  constexpr int kRowBytes = kChunkN * (int)sizeof(T);
+  constexpr int kBaseBytes = kTileRows * kRowBytes;
+  constexpr int kStepBytes = kBaseBytes + kChunkN * kPitch;
+  constexpr int kPieces = RP / 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* base = static_cast<const T*>(l.base);
   T* out = static_cast<T*>(l.out);
-  const int s0 = run * steps_per_run, steps = (l.N + kChunkN - 1) / kChunkN;
-  const int s1 = s0 + steps_per_run < steps ? s0 + steps_per_run : steps;
-  if (tl.x < 0) {  // rows without an adapter
-    if (l.base == l.out) return;
-    const int n0 = s0 * kChunkN, n1 = s1 * kChunkN < l.N ? s1 * kChunkN : l.N;
-    const int vecs = (n1 - n0) / kVec;
-    for (int i = tid; i < tl.z * vecs; i += 256) {
-      const int64_t r = p.order[tl.y + i / vecs];
-      const int n = n0 + i % vecs * kVec;
-      *reinterpret_cast<uint4*>(out + r * l.out_stride + n) =
-          *reinterpret_cast<const uint4*>(base + r * l.base_stride + n);
-    }
-    return;
-  }
-  const uint32_t t_at = smem_addr(smem), b_at = t_at + kParts * kTileRows * kPitch;
-  constexpr int kStepBytes = kChunkN * kPitch;
-  // this thread's pieces of a step of b: the shared address and the column of each
-  constexpr int kPieces = RP / 8, kMine = kChunkN * kPieces / 256;
-  uint32_t b_dst[kMine];
-  int b_col[kMine];
-#pragma unroll
-  for (int i = 0; i < kMine; ++i) {
-    const int q = tid + 256 * i, n = q / kPieces;
-    // column n = 8 kWide G + 2 kWide c + 2 w + e sits at row 8 kWide G + 8 w + 2 c + e
-    const int row = n / (8 * kWide) * (8 * kWide) + (n % (2 * kWide)) / 2 * 8 +
-                    (n % (8 * kWide)) / (2 * kWide) * 2 + (n & 1);
-    b_dst[i] = b_at + row * kPitch + q % kPieces * 16;
-    b_col[i] = n;
-  }
+  const int steps = (l.N + kChunkN - 1) / kChunkN;
+  const int64_t units = (int64_t)*p.count * steps;
+  int64_t unit = units * blockIdx.x / gridDim.x;
+  const int64_t end = units * (blockIdx.x + 1) / gridDim.x;
+  const uint32_t t_at = smem_addr(smem), ring = t_at + kParts * kTileRows * kPitch;
+  // this thread's pieces of a step: of base, rows `brow` + kRowStep i at one 16-byte column;
+  // of b, columns (rows of b) q / kPieces at one 16-byte piece
+  constexpr int kRowPieces = kRowBytes / 16, kRowStep = 256 / kRowPieces, kBase = kTileRows / kRowStep;
+  const int brow = tid / kRowPieces, bpiece = tid % kRowPieces;
+  // rows of odd number have the halves of their 128 bytes swapped: two rows' pieces fall on
+  // distinct banks when a quarter of a warp reads them
+  const uint32_t base_dst = ring + brow * kRowBytes + ((bpiece ^ ((brow & 1) << 2)) << 4);
+  constexpr int kB = (kChunkN * kPieces + 255) / 256;
   const int b_piece = tid % kPieces * 8;
-  const bool b_in = b_piece < l.rank;
-  const uint16_t* bg = l.b + (int64_t)tl.x * l.N * l.rank + b_piece;
-  auto load_b = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      const int col = s * kChunkN + b_col[i];
-      const bool in = b_in && s < s1 && col < l.N;
-      copy16(b_dst[i] + (s & 1) * kStepBytes, in ? bg + (int64_t)col * l.rank : l.b, in);
-    }
-    copies_end();
-  };
-  load_b(s0);
-  // t: the slices in order, the scale, the parts. All of a thread's loads of four ranks go out
-  // together.
-  const float scale = l.scale ? l.scale[tl.x] : 1.f;
-#pragma unroll 2
-  for (int i = tid; i < kTileRows * RP / 4; i += 256) {
-    const int r = i / (RP / 4), c = (i - r * (RP / 4)) * 4;
-    const float* src = p.part + (int64_t)(tl.y + r) * RP + c;
-    float4 q[kMaxSlices];
-#pragma unroll
-    for (int s = 0; s < kMaxSlices; ++s) {
-      q[s] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r < tl.z && s < slices) q[s] = *reinterpret_cast<const float4*>(src + (int64_t)s * l.R * RP);
-    }
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int s = 0; s < kMaxSlices; ++s) {
-      v[0] += q[s].x;
-      v[1] += q[s].y;
-      v[2] += q[s].z;
-      v[3] += q[s].w;
-    }
-#pragma unroll
-    for (int n = 0; n < 4; ++n) v[n] *= scale;
-#pragma unroll
-    for (int part = 0; part < kParts; ++part) {
-      const uint2 both = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
-      *reinterpret_cast<uint2*>(smem + (part * kTileRows + r) * kPitch + c * 2) = both;
-      v[0] -= lo(both.x);
-      v[1] -= hi(both.x);
-      v[2] -= lo(both.y);
-      v[3] -= hi(both.y);
-    }
-  }
-  const int wr = (warp & 3) * 16, wc = (warp >> 2) * 64;
+  const int wr = (warp & 3) * 16, wc = (warp >> 2) * 32;
   const int r0 = wr + (lane >> 2), r1 = r0 + 8;
-  const bool in0 = r0 < tl.z, in1 = r1 < tl.z;
-  const int64_t g0 = in0 ? p.order[tl.y + r0] : 0, g1 = in1 ? p.order[tl.y + r1] : 0;
-  constexpr int kGroups = 64 / (8 * kWide);
-  // base is read a step ahead, into the registers that the step before has just stored
-  const T* from[2] = {base + g0 * l.base_stride, base + g1 * l.base_stride};
-  T* to[2] = {out + g0 * l.out_stride, out + g1 * l.out_stride};
-  const bool in_row[2] = {in0, in1};
-  uint4 was[2][kGroups];
-  int col0 = s0 * kChunkN + wc + (lane & 3) * kVec;
+  constexpr bool kKeep = RP <= 64;  // t's fragments stay in registers
+  uint32_t kept[kKeep ? RP / 16 : 1][kParts][4];
+  const uint32_t t_row = t_at + (wr + (lane & 15)) * kPitch + (lane >> 4) * 16;
+  const uint32_t b_row = kBaseBytes + (wc + (lane & 7) + ((lane >> 4) << 3)) * kPitch + ((lane >> 3) & 1) * 16;
+  constexpr int kGroups = 32 / (8 * kWide);
+  while (unit < end) {
+    const int tile = (int)(unit / steps), first = (int)(unit - (int64_t)tile * steps);
+    const int last = end - unit < steps - first ? first + (int)(end - unit) : steps;
+    unit += last - first;
+    const int4 tl = p.tiles[tile];
+    if (tl.x < 0) {  // rows without an adapter
+      if (l.base == l.out) continue;
+      const int n0 = first * kChunkN, n1 = last * kChunkN < l.N ? last * kChunkN : l.N;
+      for (int i = warp; i < tl.z; i += 8) {
+        const int64_t r = p.order[tl.y + i];
+        for (int n = n0 + lane * kVec; n < n1; n += 32 * kVec)
+          *reinterpret_cast<uint4*>(out + r * l.out_stride + n) =
+              *reinterpret_cast<const uint4*>(base + r * l.base_stride + n);
+      }
+      continue;
+    }
+    const T* from[kBase];
+    bool row_in[kBase];
 #pragma unroll
-  for (int g = 0; g < kGroups; ++g)
+    for (int i = 0; i < kBase; ++i) {
+      const int r = brow + kRowStep * i;
+      row_in[i] = r < tl.z;
+      from[i] = base + (row_in[i] ? (int64_t)p.order[tl.y + r] * l.base_stride : 0) + bpiece * kVec;
+    }
+    const bool in_row[2] = {r0 < tl.z, r1 < tl.z};
+    T* to[2] = {out + (in_row[0] ? (int64_t)p.order[tl.y + r0] * l.out_stride : 0),
+                out + (in_row[1] ? (int64_t)p.order[tl.y + r1] * l.out_stride : 0)};
+    const uint16_t* bg = l.b + (int64_t)tl.x * l.N * l.rank + b_piece;
+    auto load = [&](int s, int stage) {
+      const bool in = s < last;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (in_row[h] && col0 + g * 8 * kWide < l.N)
-        was[h][g] = *reinterpret_cast<const uint4*>(from[h] + col0 + g * 8 * kWide);
-  for (int s = s0; s < s1; ++s, col0 += kChunkN) {
-    copies_wait<0>();
-    __syncthreads();
-    load_b(s + 1);
-    float acc[8][4];
+      for (int i = 0; i < kB; ++i) {
+        const int n = (tid + 256 * i) / kPieces;
+        if (kChunkN * kPieces % 256 && n >= kChunkN) break;
+        // column n = 8 kWide G + 2 kWide c + 2 w + e sits at row 8 kWide G + 8 w + 2 c + e
+        const int row = n / (8 * kWide) * (8 * kWide) + (n % (2 * kWide)) / 2 * 8 +
+                        (n % (8 * kWide)) / (2 * kWide) * 2 + (n & 1);
+        const bool ok = in && b_piece < l.rank && s * kChunkN + n < l.N;
+        copy16(ring + stage * kStepBytes + kBaseBytes + row * kPitch + b_piece * 2,
+               ok ? bg + (int64_t)(s * kChunkN + n) * l.rank : l.b, ok);
+      }
+      const int col = s * kChunkN + bpiece * kVec;
 #pragma unroll
-    for (int n = 0; n < 8; ++n)
+      for (int i = 0; i < kBase; ++i) {
+        const bool ok = in && row_in[i] && col < l.N;
+        copy16(base_dst + stage * kStepBytes + i * kRowStep * kRowBytes,
+               ok ? static_cast<const void*>(from[i] + s * kChunkN) : l.b, ok);
+      }
+      copies_end();
+    };
+    __syncthreads();  // the tile before is done with the shared memory
+    const uint16_t* t = p.t + (int64_t)tile * kParts * kTileRows * RP;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-    const uint32_t bt = b_at + (s & 1) * kStepBytes;
+    for (int i = 0; i < (kParts * kTileRows * kPieces + 255) / 256; ++i) {
+      const int q = tid + 256 * i, row = q / kPieces;  // rows of all parts, one after another
+      if (q < kParts * kTileRows * kPieces) copy16(t_at + row * kPitch + q % kPieces * 16, t + q * 8, true);
+    }
 #pragma unroll
-    for (int kk = 0; kk < RP / 16; ++kk) {
-      uint32_t tf[kParts][4];
+    for (int i = 0; i < kAhead; ++i) load(first + i, i);
+    int stage = 0, col0 = first * kChunkN + wc + (lane & 3) * kVec;
+    for (int s = first; s < last; ++s, col0 += kChunkN) {
+      copies_wait<kAhead - 1>();
+      __syncthreads();
+      load(s + kAhead, stage == 0 ? kAhead : stage - 1);
+      if constexpr (kKeep) {
+        if (s == first) {
 #pragma unroll
-      for (int part = 0; part < kParts; ++part)
-        ldsm4(tf[part], t_at + (part * kTileRows + wr + (lane & 15)) * kPitch + kk * 32 + (lane >> 4) * 16);
+          for (int kk = 0; kk < RP / 16; ++kk)
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        uint32_t bf[4];
-        ldsm4(bf, bt + (wc + n * 16 + (lane & 7) + ((lane >> 4) << 3)) * kPitch + kk * 32 +
-                      ((lane >> 3) & 1) * 16);
-#pragma unroll
-        for (int part = kParts - 1; part >= 0; --part) {
-          mma(acc[2 * n], tf[part], bf[0], bf[1]);
-          mma(acc[2 * n + 1], tf[part], bf[2], bf[3]);
+            for (int part = 0; part < kParts; ++part)
+              ldsm4(kept[kk][part], t_row + part * kTileRows * kPitch + kk * 32);
         }
       }
-    }
-    const int ahead = s + 1 < s1 ? kChunkN : l.N;
+      const uint32_t at = ring + stage * kStepBytes;
+      // one 16-byte access's columns at a time
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      const int col = col0 + g * 8 * kWide;
+      for (int g = 0; g < kGroups; ++g) {
+        float acc[kWide][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (in_row[h] && col < l.N) {
+        for (int w = 0; w < kWide; ++w)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[w][i] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < RP / 16; ++kk) {
+          uint32_t tf[kParts][4];
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) {
+            if constexpr (kKeep) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) tf[part][i] = kept[kk][part][i];
+            } else {
+              ldsm4(tf[part], t_row + part * kTileRows * kPitch + kk * 32);
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < kWide; w += 2) {
+            uint32_t bf[4];
+            ldsm4(bf, at + b_row + (g * kWide + w) * 8 * kPitch + kk * 32);
+#pragma unroll
+            for (int part = kParts - 1; part >= 0; --part) {
+              mma(acc[w], tf[part], bf[0], bf[1]);
+              mma(acc[w + 1], tf[part], bf[2], bf[3]);
+            }
+          }
+        }
+        const int col = col0 + g * 8 * kWide;
+        if (col >= l.N) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!in_row[h]) continue;
+          const int row = h ? r1 : r0, piece = (wc + g * 8 * kWide) / kVec + (lane & 3);
+          const uint4 was = *reinterpret_cast<const uint4*>(
+              smem + (at - t_at) + row * kRowBytes + ((piece ^ ((row & 1) << 2)) << 4));
           float f[kVec];
-          Vec<T>::get(was[h][g], f);
+          Vec<T>::get(was, f);
 #pragma unroll
           for (int w = 0; w < kWide; ++w) {
-            f[2 * w] += acc[g * kWide + w][2 * h];
-            f[2 * w + 1] += acc[g * kWide + w][2 * h + 1];
+            f[2 * w] += acc[w][2 * h];
+            f[2 * w + 1] += acc[w][2 * h + 1];
           }
           *reinterpret_cast<uint4*>(to[h] + col) = Vec<T>::put(f);
         }
-        if (in_row[h] && col + ahead < l.N)
-          was[h][g] = *reinterpret_cast<const uint4*>(from[h] + col + ahead);
       }
+      stage = stage == kAhead ? 0 : stage + 1;
     }
+    copies_wait<0>();
   }
-  copies_wait<0>();
 }
 
 int rank_pad(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
@@ -670,8 +725,8 @@ Plan plan_at(const Lora& l, void* ws, size_t* end) {
   at += up256((size_t)max_tiles(l.R, l.G) * 16);
   p.order = reinterpret_cast<int32_t*>(at);
   at += up256((size_t)l.R * 4);
-  p.part = reinterpret_cast<float*>(at);
-  at += up256((size_t)feature_slices(l) * l.R * rank_pad(l.rank) * 4);
+  p.t = reinterpret_cast<uint16_t*>(at);
+  at += up256((size_t)max_tiles(l.R, l.G) * (l.fp32 ? 3 : 2) * kTileRows * rank_pad(l.rank) * 2);
   *end = (size_t)(at - static_cast<char*>(ws));
   return p;
 }
@@ -690,23 +745,21 @@ cudaError_t run_tiles(const Lora& l, const Plan& p, cudaStream_t st) {
   const size_t shrink_smem = (size_t)kStages * (kTileRows + RP) * kChunkK * 2;
   cudaError_t e = allow_smem(k_shrink_tiles<RP>, shrink_smem);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k_shrink_tiles<RP>, dim3((unsigned)(tiles * slices)), dim3(128), shrink_smem, st, l,
-                 p, slices);
+  e = launch_cluster(k_shrink_tiles<RP>, (unsigned)(tiles * slices), 128, shrink_smem,
+                     (unsigned)slices, st, l, p, slices);
   if (e != cudaSuccess) return e;
-  const int steps = (l.N + kChunkN - 1) / kChunkN;
-  const int per = steps < 8 ? steps : 8;
-  const int runs = (steps + per - 1) / per;
-  const int parts = l.fp32 ? 3 : 2;
-  const size_t smem = (size_t)(parts * kTileRows + 2 * kChunkN) * (RP * 2 + 16);
-  const dim3 grid((unsigned)(tiles * runs)), block(256);
+  const int parts = l.fp32 ? 3 : 2, size = l.fp32 ? 4 : 2;
+  const size_t smem = (size_t)parts * kTileRows * (RP * 2 + 16) +
+                      (size_t)(kAhead + 1) * kChunkN * (kTileRows * size + RP * 2 + 16);
+  const dim3 grid((unsigned)(num_sms() * (RP <= 64 ? 2 : 1))), block(256);
   if (l.fp32) {
     e = allow_smem(k_expand_tiles<float, RP>, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_expand_tiles<float, RP>, grid, block, smem, st, l, p, slices, runs, per);
+    return launch_pdl(k_expand_tiles<float, RP>, grid, block, smem, st, l, p);
   }
   e = allow_smem(k_expand_tiles<__nv_bfloat16, RP>, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_expand_tiles<__nv_bfloat16, RP>, grid, block, smem, st, l, p, slices, runs, per);
+  return launch_pdl(k_expand_tiles<__nv_bfloat16, RP>, grid, block, smem, st, l, p);
 }
 
 }  // namespace
