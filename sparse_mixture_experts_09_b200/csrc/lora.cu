@@ -575,11 +575,22 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
     if (tl.x < 0) {  // rows without an adapter
       if (l.base == l.out) continue;
       const int n0 = first * kChunkN, n1 = last * kChunkN < l.N ? last * kChunkN : l.N;
-      for (int i = warp; i < tl.z; i += 8) {
-        const int64_t r = p.order[tl.y + i];
-        for (int n = n0 + lane * kVec; n < n1; n += 32 * kVec)
-          *reinterpret_cast<uint4*>(out + r * l.out_stride + n) =
-              *reinterpret_cast<const uint4*>(base + r * l.base_stride + n);
+      const int vecs = (n1 - n0) / kVec, all = vecs * tl.z;
+      for (int i0 = tid; i0 < all; i0 += 256 * 4) {  // four pieces of a thread in flight
+        uint4 v[4];
+        int64_t at[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int i = i0 + 256 * q;
+          if (i >= all) continue;
+          const int64_t r = p.order[tl.y + i / vecs];
+          const int n = n0 + i % vecs * kVec;
+          at[q] = r * l.out_stride + n;
+          v[q] = *reinterpret_cast<const uint4*>(base + r * l.base_stride + n);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (i0 + 256 * q < all) *reinterpret_cast<uint4*>(out + at[q]) = v[q];
       }
       continue;
     }
@@ -698,20 +709,30 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
 
 int rank_pad(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
 
-// Rows from which the tiles are used.
-constexpr int64_t kTilesFrom = 128;
+// Whether the rows go by tiles. A row on its own streams its adapter again for every row; a
+// tile costs as much for one row as for 64, and the sorting and two more launches some 8 us.
+// Device times, rows / tiles: 64 rows of 4 adapters, rank 64, 4096 -> 14336 features 27 / 20 us,
+// of 64 adapters 36 / 67; 128 rows of 8 adapters, rank 16, 4096 -> 4096 11 / 14 us; 256 rows of 8
+// adapters 20 / 15, of 256 adapters 23 / 41. How many adapters a batch uses is not known here:
+// from 128 rows on the tiles lose less in their worst case than they gain in their best.
+bool use_tiles(const Lora& l) {
+  const int64_t adapter_bytes = (int64_t)l.rank * (l.H + l.N) * 2;
+  return l.R >= 128 || (l.R >= 12 * (int64_t)l.G && l.R * adapter_bytes >= (int64_t)64 << 20);
+}
 
 // Slices of the features: as many blocks as the SMs hold at once (three each; a second
-// round for a few blocks would double the time), at least two stages each. How many tiles
-// the adapters leave partly filled is not known here; twice the full ones is the most
-// allowed for.
+// round for a few blocks would double the time), at least two stages each, and a power of
+// two, as clusters of 5 to 7 blocks leave SMs empty: 4096 rows, rank 64, 4096 features
+// 31 / 20 / 19 / 19 / 28 us at 1 / 2 / 4 / 6 / 8 slices, rank 128 51 / 31 / 27 / 40 / 44 us. How
+// many tiles the adapters leave partly filled is not known here; twice the full ones is
+// the most allowed for.
 int feature_slices(const Lora& l) {
   const int64_t full = (l.R + kTileRows - 1) / kTileRows, most = max_tiles(l.R, l.G);
   const int64_t tiles = most < 2 * full ? most : 2 * full;
   const int64_t chunks = (l.H + kChunkK - 1) / kChunkK;
   int64_t s = (int64_t)num_sms() * 3 / tiles;
   if (s > chunks / 2) s = chunks / 2;
-  return s < 1 ? 1 : s > kMaxSlices ? kMaxSlices : (int)s;
+  return s >= 8 ? 8 : s >= 4 ? 4 : s >= 2 ? 2 : 1;
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -765,14 +786,14 @@ cudaError_t run_tiles(const Lora& l, const Plan& p, cudaStream_t st) {
 }  // namespace
 
 size_t lora_workspace(const Lora& l) {
-  if (l.R < kTilesFrom) return 0;
+  if (!use_tiles(l)) return 0;
   size_t end = 0;
   plan_at(l, nullptr, &end);
   return end;
 }
 
 cudaError_t launch_lora(const Lora& l, void* ws, cudaStream_t st) {
-  if (l.R >= kTilesFrom) {
+  if (use_tiles(l)) {
     size_t end = 0;
     const Plan p = plan_at(l, ws, &end);
     const size_t smem = (size_t)(l.G + 1) * 4;
