@@ -489,6 +489,18 @@ typedef struct {
 moe_status_t moe_route(const moe_routing_t* routing, const void* logits, const float* select_bias,
                        int32_t* topk_idx, float* topk_w, moe_stream_t stream);
 
+/* moe_forward with the routing above in place of Mixtral's: the router's logits (fp32, or
+ * rounded to bf16 as shape->router_bf16_logits asks; logit_bias added), moe_route, then the
+ * layer's permutation, experts and combine. routing: num_tokens, num_experts and
+ * num_experts_per_tok equal the shape's (so at most 64 experts and 8 slots), logits_bf16 = 0,
+ * logits_stride = num_experts. select_bias [E] fp32 and logit_bias [E] fp32 nullable. */
+moe_status_t moe_forward_routing(const moe_shape_t* shape, const moe_routing_t* routing,
+                                 const moe_bf16_t* x, const moe_bf16_t* w_router,
+                                 const float* logit_bias, const float* select_bias,
+                                 const moe_bf16_t* w1, const moe_bf16_t* w3, const moe_bf16_t* w2,
+                                 const moe_bf16_t* residual, moe_bf16_t* out, void* ws,
+                                 size_t ws_bytes, moe_stream_t stream);
+
 /* Router losses over the N tokens whose token_mask is non-zero:
  *   p = softmax(l), or s / sum(s) with sigmoid scores;   P_e = sum_t p_te / N
  *   f_e = counts_e / N, counts_e the slots of those tokens that name expert e
@@ -576,6 +588,28 @@ moe_status_t moe_lora_add(const moe_lora_t* lora, const void* base, const moe_bf
                           const moe_bf16_t* a, const moe_bf16_t* b, const int32_t* adapter,
                           const float* scale, void* out, void* ws, size_t ws_bytes,
                           moe_stream_t stream);
+
+/* Adapter of every routed row, for adapters per request and expert [num_adapters, E]:
+ *   row_adapter[r] = adapter[t] * E + e  for a row of token t in expert e's group,
+ *   -1 for a pad row, a row past the last group (up to num_rows), and a token whose adapter
+ *   is outside [0, num_adapters).
+ *   token_of_row [num_rows] and expert_offsets [E + 1] int32 as moe_permute writes them;
+ *   adapter [T] int32, T = num_tokens (a token_of_row outside [0, T) is no row);
+ *   row_adapter [num_rows] int32 out. 1 <= num_experts <= 512, num_rows >= 0,
+ *   num_adapters * num_experts <= 16384. */
+moe_status_t moe_lora_rows(const int32_t* token_of_row, const int32_t* expert_offsets,
+                           const int32_t* adapter, int64_t num_tokens, int64_t num_rows,
+                           int num_experts, int num_adapters, int32_t* row_adapter,
+                           moe_stream_t stream);
+
+/* The experts' activation on its own, for projections that something is added to before it:
+ *   h = bf16(silu(gate) * up), silu(g) = g / (1 + exp(-g)), for the rows below
+ *   expert_offsets[E] (rows past them untouched).
+ *   gate, up [num_rows, I] fp32; h [num_rows, I] bf16 out; I a positive multiple of 8;
+ *   expert_offsets [E + 1] int32; 16-byte aligned; num_rows >= 0. */
+moe_status_t moe_swiglu_rows(const float* gate, const float* up, const int32_t* expert_offsets,
+                             int num_experts, int64_t num_rows, int intermediate, moe_bf16_t* h,
+                             moe_stream_t stream);
 
 /* Waits for `stream`, then reads and clears the device status word in `ws`:
  * MOE_OK, or MOE_ERR_TIMEOUT if a kernel gave up a bounded wait since the last

@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe.so")
 SOURCES = ["moe_api.cu", "routing.cu", "gemm_sm100.cu", "gemm_w8.cu", "combine.cu", "moe_noalloc.cu",
            "gather_rows.cu", "ep_peer.cu", "route.cu", "combine_bwd.cu",
-           "lora.cu", "router_adapter_api.cu"]
+           "lora.cu", "swiglu_rows.cu", "router_adapter_api.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

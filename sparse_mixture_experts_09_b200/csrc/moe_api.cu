@@ -50,7 +50,7 @@ inline size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 // Workspace regions, in order; each starts on a 1024-byte boundary.
 struct Layout {
   size_t status, topk_idx, topk_w, block_base, counts, offsets, row_of, token_of_row, x_perm, h,
-      y, rnorm, row_ready, split_sem, partial, end;
+      y, rnorm, row_ready, logits, split_sem, partial, end;
   size_t x_in[2], res_in[2], out_st, end_host;  // staging of the host entry points
 };
 
@@ -72,6 +72,7 @@ Layout layout(const Shape& s) {
   L.y = o; o += up(rmax * s.H * 4);
   L.rnorm = o; o += up((size_t)s.T * 4);
   L.row_ready = o; o += up((size_t)(rmax / 64) * 4);  // one-grid experts: sub-tiles of h done
+  L.logits = o; o += up((size_t)s.T * s.E * 4);  // of moe_forward_routing
   // split-K of the down GEMM (small batches only): arrival counters and partial sums
   const bool split = (int64_t)tk <= kSplitMaxRows;
   L.split_sem = o; o += split ? up((size_t)kSplitSems * 4) : 0;
@@ -262,12 +263,18 @@ moe_status_t run_experts(const Shape& s, const uint16_t* x_perm, const int32_t* 
 
 moe_status_t run_forward(const Shape& s, const uint16_t* x, const uint16_t* wr, const float* bias,
                          const Experts& w, const uint16_t* res, uint16_t* out, void* ws,
-                         cudaStream_t st, const uint16_t* norm_w = nullptr, float eps = 0.f) {
+                         cudaStream_t st, const uint16_t* norm_w = nullptr, float eps = 0.f,
+                         const Routing* routing = nullptr, const float* select_bias = nullptr) {
   const Layout L = layout(s);
   float* rnorm = norm_w ? at<float>(ws, L.rnorm) : nullptr;
   cudaError_t e = launch_router(s, x, wr, bias, at<int32_t>(ws, L.topk_idx), at<float>(ws, L.topk_w),
-                                nullptr, st, norm_w, eps, rnorm);
+                                routing ? at<float>(ws, L.logits) : nullptr, st, norm_w, eps, rnorm);
   if (e != cudaSuccess) return cuda_fail(e, "router launch");
+  if (routing) {  // the router's own choice is replaced
+    e = launch_route(*routing, at<float>(ws, L.logits), select_bias, at<int32_t>(ws, L.topk_idx),
+                     at<float>(ws, L.topk_w), st);
+    if (e != cudaSuccess) return cuda_fail(e, "routing launch");
+  }
   e = launch_permute(s, at<int32_t>(ws, L.topk_idx), x, at<int32_t>(ws, L.counts),
                      at<int32_t>(ws, L.offsets), at<int32_t>(ws, L.row_of),
                      at<int32_t>(ws, L.token_of_row), at<uint16_t>(ws, L.x_perm),
@@ -583,6 +590,35 @@ moe_status_t moe_forward_rmsnorm(const moe_shape_t* shape, const moe_bf16_t* h,
   MOE_TRY(check_ws(ws, ws_bytes, layout(s).end));
   return run_forward(s, h, w_router, logit_bias, bf16_experts(w1, w3, w2), h, out, ws,
                      (cudaStream_t)stream, norm_weight, eps);
+}
+
+moe_status_t moe_forward_routing(const moe_shape_t* shape, const moe_routing_t* routing,
+                                 const moe_bf16_t* x, const moe_bf16_t* w_router,
+                                 const float* logit_bias, const float* select_bias,
+                                 const moe_bf16_t* w1, const moe_bf16_t* w3, const moe_bf16_t* w2,
+                                 const moe_bf16_t* residual, moe_bf16_t* out, void* ws,
+                                 size_t ws_bytes, moe_stream_t stream) {
+  g_err[0] = 0;
+  Shape s;
+  Routing r;
+  MOE_TRY(check_shape(shape, &s));
+  MOE_TRY(check_routing(routing, true, &r));
+  if (r.T != s.T || r.E != s.E || r.k != s.k)
+    return fail(MOE_ERR_INVALID_ARG, "routing's num_tokens, num_experts and num_experts_per_tok must be the shape's");
+  if (r.bf16 || r.stride != s.E)
+    return fail(MOE_ERR_INVALID_ARG, "routing must have logits_bf16 = 0 and logits_stride = num_experts");
+  MOE_TRY(check_ptr(x, "x"));
+  MOE_TRY(check_ptr(w_router, "w_router"));
+  MOE_TRY(check_ptr(logit_bias, "logit_bias", true));
+  MOE_TRY(check_ptr(select_bias, "select_bias", true));
+  MOE_TRY(check_ptr(w1, "w1"));
+  MOE_TRY(check_ptr(w3, "w3"));
+  MOE_TRY(check_ptr(w2, "w2"));
+  MOE_TRY(check_ptr(residual, "residual", true));
+  MOE_TRY(check_ptr(out, "out"));
+  MOE_TRY(check_ws(ws, ws_bytes, layout(s).end));
+  return run_forward(s, x, w_router, logit_bias, bf16_experts(w1, w3, w2), residual, out, ws,
+                     (cudaStream_t)stream, nullptr, 0.f, &r, select_bias);
 }
 
 moe_status_t moe_forward_host(const moe_shape_t* shape, const moe_bf16_t* x_host,

@@ -228,6 +228,13 @@ struct Lora {
   const void* base;
   void* out;
 };
+// The experts' activation and the routed rows' adapters (swiglu_rows.cu).
+cudaError_t launch_swiglu_rows(const float* gate, const float* up, const int32_t* offsets, int E,
+                               int64_t rows, int I, uint16_t* h, cudaStream_t st);
+cudaError_t launch_lora_rows(const int32_t* token_of_row, const int32_t* offsets,
+                             const int32_t* adapter, int64_t T, int64_t rows, int E, int G,
+                             int32_t* row_adapter, cudaStream_t st);
+
 size_t lora_workspace(const Lora& l);
 cudaError_t launch_lora(const Lora& l, void* ws, cudaStream_t st);
 
@@ -243,6 +250,8 @@ void set_error_message(const char* msg);
 moe_status_t fail_with(moe_status_t code, const char* fmt, ...);
 moe_status_t launched(cudaError_t e, const char* where);
 moe_status_t check_aligned(const void* p, const char* name, size_t align, bool nullable);
+// moe_routing_t -> Routing; full: the selection rule is checked too.
+moe_status_t check_routing(const moe_routing_t* in, bool full, Routing* out);
 
 // ---- programmatic dependent launch ----
 // Every kernel of the layer is launched with programmatic stream serialization: it

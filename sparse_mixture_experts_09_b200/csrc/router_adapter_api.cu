@@ -34,7 +34,6 @@ moe_status_t check_aligned(const void* p, const char* name, size_t align, bool n
   return MOE_OK;
 }
 
-// moe_routing_t -> Routing. full: the selection rule is checked too.
 moe_status_t check_routing(const moe_routing_t* in, bool full, Routing* out) {
   if (!in) return fail_with(MOE_ERR_INVALID_ARG, "routing is NULL");
   if (in->num_tokens < 0 || in->num_tokens > (int64_t)1 << 30)
@@ -300,6 +299,50 @@ moe_status_t moe_lora_add(const moe_lora_t* lora, const void* base, const moe_bf
   l.base = base;
   l.out = out;
   return launched(launch_lora(l, ws, (cudaStream_t)stream), "adapter launch");
+}
+
+moe_status_t moe_lora_rows(const int32_t* token_of_row, const int32_t* expert_offsets,
+                           const int32_t* adapter, int64_t num_tokens, int64_t num_rows,
+                           int num_experts, int num_adapters, int32_t* row_adapter,
+                           moe_stream_t stream) {
+  set_error_message("");
+  if (num_tokens < 0 || num_rows < 0 || num_rows > INT_MAX)
+    return fail_with(MOE_ERR_INVALID_ARG, "num_tokens and num_rows must be in [0, 2^31)");
+  if (num_experts < 1 || num_experts > 512)
+    return fail_with(MOE_ERR_UNSUPPORTED, "num_experts must be in [1, 512] (got %d)", num_experts);
+  if (num_adapters < 1 || num_adapters > 16384 / num_experts)
+    return fail_with(MOE_ERR_UNSUPPORTED,
+                     "num_adapters must be >= 1 and num_adapters * num_experts <= 16384 (got %d)",
+                     num_adapters);
+  if (num_rows == 0) return MOE_OK;
+  MOE_TRY(check_aligned(token_of_row, "token_of_row", 4, false));
+  MOE_TRY(check_aligned(expert_offsets, "expert_offsets", 4, false));
+  MOE_TRY(check_aligned(adapter, "adapter", 4, num_tokens == 0));
+  MOE_TRY(check_aligned(row_adapter, "row_adapter", 4, false));
+  return launched(launch_lora_rows(token_of_row, expert_offsets, adapter, num_tokens, num_rows,
+                                   num_experts, num_adapters, row_adapter, (cudaStream_t)stream),
+                  "row adapter launch");
+}
+
+moe_status_t moe_swiglu_rows(const float* gate, const float* up, const int32_t* expert_offsets,
+                             int num_experts, int64_t num_rows, int intermediate, moe_bf16_t* h,
+                             moe_stream_t stream) {
+  set_error_message("");
+  if (num_rows < 0 || num_rows > INT_MAX)
+    return fail_with(MOE_ERR_INVALID_ARG, "num_rows must be in [0, 2^31)");
+  if (num_experts < 1 || num_experts > 512)
+    return fail_with(MOE_ERR_UNSUPPORTED, "num_experts must be in [1, 512] (got %d)", num_experts);
+  if (intermediate <= 0 || intermediate % 8)
+    return fail_with(MOE_ERR_UNSUPPORTED, "intermediate must be a positive multiple of 8 (got %d)",
+                     intermediate);
+  if (num_rows == 0) return MOE_OK;
+  MOE_TRY(check_aligned(gate, "gate", 16, false));
+  MOE_TRY(check_aligned(up, "up", 16, false));
+  MOE_TRY(check_aligned(expert_offsets, "expert_offsets", 4, false));
+  MOE_TRY(check_aligned(h, "h", 16, false));
+  return launched(launch_swiglu_rows(gate, up, expert_offsets, num_experts, num_rows, intermediate, h,
+                                     (cudaStream_t)stream),
+                  "activation launch");
 }
 
 }  // extern "C"

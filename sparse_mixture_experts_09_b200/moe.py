@@ -32,7 +32,7 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_size_host", "moe_max_padded_rows
            "moe_ipc_alloc", "moe_ipc_open", "moe_ipc_close", "moe_ipc_free",
            "moe_scatter_rows_peer", "moe_combine_peer", "moe_route", "moe_router_losses",
            "moe_router_losses_workspace", "moe_route_backward", "moe_combine_backward",
-           "moe_lora_workspace", "moe_lora_add")
+           "moe_lora_workspace", "moe_lora_add", "moe_lora_rows", "moe_swiglu_rows", "moe_forward_routing")
 
 
 @dataclass
@@ -201,6 +201,13 @@ def lib() -> ctypes.CDLL:
         L.moe_lora_workspace.restype = _SZ
         L.moe_lora_add.argtypes = [lp] + [_P] * 8 + [_SZ, _P]
         L.moe_lora_add.restype = st
+        L.moe_lora_rows.argtypes = [_P, _P, _P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                                    ctypes.c_int, _P, _P]
+        L.moe_lora_rows.restype = st
+        L.moe_swiglu_rows.argtypes = [_P, _P, _P, ctypes.c_int, ctypes.c_int64, ctypes.c_int, _P, _P]
+        L.moe_swiglu_rows.restype = st
+        L.moe_forward_routing.argtypes = [sp, rp] + [_P] * 10 + [_SZ, _P]
+        L.moe_forward_routing.restype = st
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         _lib = L
@@ -857,6 +864,37 @@ def route(logits, routing: Routing, bias=None, stream=None):
     return _on(dev, stream, call)
 
 
+def forward_routing(x, w_router, w1, w3, w2, routing: Routing, bias=None, residual=None,
+                    logit_bias=None, ws=None, out=None, stream=None, weight_layout: int = ROW_MAJOR,
+                    router_bf16_logits: bool = False):
+    """forward with `routing` (and its selection bias [E] fp32) in place of Mixtral's rule;
+    returns out [T,H] bf16."""
+    t, h = x.shape
+    e, i, _ = w1.shape
+    shape = make_shape(t, h, i, e, routing.k, weight_layout, router_bf16_logits)
+    if routing.scoring not in _SCORING:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {routing.scoring!r}")
+    args = _RoutingArgs(t, e, e, routing.k, _SCORING[routing.scoring], routing.num_groups,
+                        routing.topk_groups, routing.group_top, int(routing.renormalize), 0,
+                        routing.scale)
+    _layer_sizes(t, h, e, i, w_router, logit_bias, residual, out, bias=(bias, e),
+                 **_bf16_weights(e, i, h, w1, w3, w2))
+    xp = _dev(x, "x", torch.bfloat16)
+
+    def call(st):
+        work = make_workspace(shape, x.device) if ws is None else ws
+        dst = torch.empty(t, h, dtype=torch.bfloat16, device=x.device) if out is None else out
+        _check(lib().moe_forward_routing(
+            shape, args, xp, _dev(w_router, "w_router", torch.bfloat16),
+            _dev(logit_bias, "logit_bias", torch.float32, True), _dev(bias, "bias", torch.float32, True),
+            _dev(w1, "w1", torch.bfloat16), _dev(w3, "w3", torch.bfloat16),
+            _dev(w2, "w2", torch.bfloat16), _dev(residual, "residual", torch.bfloat16, True),
+            _dev(dst, "out", torch.bfloat16), _dev(work, "ws"), work.numel(), st))
+        return dst
+
+    return _on(x.device, stream, call)
+
+
 def _token_mask(mask, t: int, dev) -> Optional[int]:
     return None if mask is None else _arg(mask, "token_mask", (torch.bool, torch.uint8), (t,), dev)
 
@@ -974,3 +1012,119 @@ def lora_add(base, x, a, b, adapter, scale=None, out=None, stream=None):
         return dst
 
     return _on(dev, stream, call)
+
+
+@dataclass
+class LoraExperts:
+    """Low-rank adapters of every request beside every expert's projections: a1, a3
+    [L, E, rank, H], b1, b3 [L, E, I, rank] (gate and up), a2 [L, E, rank, I], b2
+    [L, E, H, rank] (down), bf16, L adapters; scale [L] fp32 or None. A pair may be None: that
+    projection has no adapters. Ranks may differ between the pairs."""
+    a1: Optional[torch.Tensor] = None
+    b1: Optional[torch.Tensor] = None
+    a3: Optional[torch.Tensor] = None
+    b3: Optional[torch.Tensor] = None
+    a2: Optional[torch.Tensor] = None
+    b2: Optional[torch.Tensor] = None
+    scale: Optional[torch.Tensor] = None
+
+
+def lora_rows(token_of_row, offsets, adapter, num_adapters: int, stream=None):
+    """Adapter of every routed row (see moe_lora_rows): adapter[token] * E + expert, or -1.
+    token_of_row and offsets are permute's; adapter [T] int32 per token."""
+    if token_of_row.dim() != 1 or offsets.dim() != 1 or adapter.dim() != 1:
+        raise ValueError("token_of_row, offsets and adapter must be 1-D")
+    rows, e, dev = token_of_row.numel(), offsets.numel() - 1, token_of_row.device
+    tp = _arg(token_of_row, "token_of_row", _I32, (rows,))
+    op = _arg(offsets, "offsets", _I32, (e + 1,), dev)
+    ap = _arg(adapter, "adapter", _I32, (adapter.numel(),), dev)
+
+    def call(st):
+        ids = torch.empty(rows, dtype=torch.int32, device=dev)
+        _check(lib().moe_lora_rows(tp, op, ap, adapter.numel(), rows, e, num_adapters, ids.data_ptr(), st))
+        return ids
+
+    return _on(dev, stream, call)
+
+
+def swiglu_rows(gate, up, offsets, h=None, stream=None):
+    """h [R, I] bf16 = bf16(silu(gate) * up) of fp32 gate and up [R, I], for the rows below
+    offsets[E] (the others of `h` are untouched)."""
+    if gate.dim() != 2:
+        raise ValueError("gate must be [rows, intermediate]")
+    rows, i = gate.shape
+    dev = gate.device
+    gp, up_p = _arg(gate, "gate", _F32, (rows, i)), _arg(up, "up", _F32, (rows, i), dev)
+    op = _arg(offsets, "offsets", _I32, (offsets.numel(),), dev)
+    hp = None if h is None else _arg(h, "h", _BF16, (rows, i), dev)
+
+    def call(st):
+        dst = torch.empty(rows, i, dtype=torch.bfloat16, device=dev) if h is None else h
+        _check(lib().moe_swiglu_rows(gp, up_p, op, offsets.numel() - 1, rows, i,
+                                     dst.data_ptr() if hp is None else hp, st))
+        return dst
+
+    return _on(dev, stream, call)
+
+
+def forward_lora(x, w_router, w1, w3, w2, k: int, adapters: LoraExperts, adapter, residual=None,
+                 logit_bias=None, stream=None, weight_layout: int = ROW_MAJOR,
+                 router_bf16_logits: bool = False, routing: Optional[Routing] = None, bias=None):
+    """The whole layer with adapter[t] (int32 [T], outside [0, L): none) beside every expert
+    projection of token t:
+        gate = w1 x + s B1 A1 x,  up = w3 x + s B3 A3 x,  h = bf16(silu(gate) * up),
+        y = w2 h + s B2 A2 h      (fp32 but h)
+    `routing` (with its selection bias) replaces Mixtral's rule when given (its k is used).
+    Returns out [T,H] bf16. The gate and up projections run as plain grouped GEMMs into
+    fp32, since the adapters come between them and the activation."""
+    t, h = x.shape
+    e, i, _ = w1.shape
+    if routing is not None:
+        k = routing.k
+    _layer_sizes(t, h, e, i, w_router, logit_bias, residual, None, adapter=(adapter, t), bias=(bias, e),
+                 **_bf16_weights(e, i, h, w1, w3, w2))
+    pairs, count = {}, 0
+    for name, a, b, n_in, n_out in (("1", adapters.a1, adapters.b1, h, i),
+                                    ("3", adapters.a3, adapters.b3, h, i),
+                                    ("2", adapters.a2, adapters.b2, i, h)):
+        if (a is None) != (b is None):
+            raise ValueError(f"a{name} and b{name} go together")
+        if a is None:
+            continue
+        if a.dim() != 4 or a.shape[1] != e or a.shape[3] != n_in:
+            raise ValueError(f"a{name} must be [L, {e}, rank, {n_in}], got {tuple(a.shape)}")
+        count = count or a.shape[0]
+        if a.shape[0] != count or tuple(b.shape) != (count, e, n_out, a.shape[2]):
+            raise ValueError(f"b{name} must be [{count}, {e}, {n_out}, {a.shape[2]}], got {tuple(b.shape)}")
+        pairs[name] = (a.reshape(count * e, a.shape[2], n_in), b.reshape(count * e, n_out, a.shape[2]))
+    if not pairs:
+        raise ValueError("adapters holds no pair")
+    _sized("scale", adapters.scale, count)
+
+    def call(st):
+        wide = make_shape(t, i, h, e, k, weight_layout)   # the gate and up GEMMs: H in, I out
+        shape = make_shape(t, h, i, e, k, weight_layout)
+        ws = make_workspace(shape if workspace_size(shape) >= workspace_size(wide) else wide, x.device)
+        rows = max_padded_rows(shape)
+        if routing is None:
+            idx, w = router_topk(x, w_router, k, logit_bias, router_bf16_logits=router_bf16_logits)
+        else:
+            logits = router_topk(x, w_router, 1, logit_bias, True, router_bf16_logits=router_bf16_logits)[2]
+            idx, w = route(logits, routing, bias)
+        perm = permute(idx, x, e, i, ws)
+        ids = lora_rows(perm["token_of_row"], perm["offsets"], adapter, count)
+        scale = None if adapters.scale is None else adapters.scale.repeat_interleave(e)
+
+        def project(rows_in, weights, n_out, name):
+            y = torch.empty(rows, n_out, dtype=torch.float32, device=x.device)
+            expert_down(rows_in, perm["offsets"], weights, t, k, ws, y=y, weight_layout=weight_layout)
+            if name in pairs:
+                lora_add(y, rows_in[:rows], *pairs[name], ids, scale, out=y)
+            return y
+
+        gate, up = project(perm["x_perm"], w1, i, "1"), project(perm["x_perm"], w3, i, "3")
+        act = swiglu_rows(gate, up, perm["offsets"])
+        y = project(act, w2, h, "2")
+        return combine(y, perm["row_of"], w, residual, e, i)
+
+    return _on(x.device, stream, call)

@@ -85,3 +85,46 @@ def test_binding_refuses():
         M.combine_backward(bf(4), torch.zeros(8, 64), ids[:, None], torch.zeros(4, 1))
     with pytest.raises(ValueError, match="CUDA"):
         M.combine_backward(bf(4, 64), torch.zeros(8, 64), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2))
+
+
+def test_layer_entry_points_refuse(L):
+    s = M.make_shape(4, 128, 128, 8, 2)
+    r = lambda **kw: M._RoutingArgs(**{**dict(num_tokens=4, logits_stride=8, num_experts=8, num_experts_per_tok=2, num_groups=1,
+                                              topk_groups=1, group_top=1, renormalize=1, weight_scale=1.0), **kw})
+    fwd = lambda routing, ws=256, size=1 << 30, x=16, bias=None: L.moe_forward_routing(
+        s, routing, x, 16, None, bias, 16, 16, 16, None, 16, ws, size, None)
+    for bad in (dict(num_tokens=5), dict(num_experts=16, logits_stride=16), dict(num_experts_per_tok=3), dict(logits_bf16=1),
+                dict(logits_stride=9), dict(num_groups=3), dict(scoring=5)):
+        assert fwd(r(**bad)) in (1, 2) and L.moe_last_error()
+    assert fwd(None) == 1 and fwd(r(), x=None) == 1 and fwd(r(), bias=8) == 1
+    assert fwd(r(), ws=None) == 3 and fwd(r(), size=1) == 3
+    rows = lambda tok=16, off=16, ad=16, t=4, n=8, e=8, g=2, out=16: L.moe_lora_rows(tok, off, ad, t, n, e, g, out, None)
+    for bad in (dict(tok=None), dict(off=None), dict(ad=None), dict(out=None), dict(t=-1), dict(n=-1), dict(e=0), dict(e=513),
+                dict(g=0), dict(g=2049), dict(out=2)):
+        assert rows(**bad) in (1, 2) and L.moe_last_error()
+    assert rows(n=0, tok=None, off=None, out=None) == 0
+    act = lambda g=16, u=16, off=16, e=8, n=4, i=64, h=16: L.moe_swiglu_rows(g, u, off, e, n, i, h, None)
+    for bad in (dict(g=None), dict(u=8), dict(off=None), dict(h=None), dict(e=0), dict(n=-1), dict(i=0), dict(i=60)):
+        assert act(**bad) in (1, 2) and L.moe_last_error()
+    assert act(n=0, g=None, u=None, off=None, h=None) == 0
+
+
+def test_layer_binding_refuses():
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    x, wr, w1, w2 = bf(4, 128), bf(8, 128), bf(8, 256, 128), bf(8, 128, 256)
+    ids = torch.zeros(4, dtype=torch.int32)
+    a, b = bf(3, 8, 16, 128), bf(3, 8, 256, 16)
+    lora = lambda ad, i=ids: M.forward_lora(x, wr, w1, w1, w2, 2, ad, i)
+    for ad, match in ((M.LoraExperts(), "no pair"), (M.LoraExperts(a1=a), "go together"), (M.LoraExperts(a1=a, b1=bf(3, 8, 128, 16)), "b1"),
+                      (M.LoraExperts(a2=a, b2=b), "a2"), (M.LoraExperts(a1=a, b1=b, scale=torch.ones(2)), "scale"),
+                      (M.LoraExperts(a1=a, b1=b, a3=bf(2, 8, 16, 128), b3=bf(2, 8, 256, 16)), "b3")):
+        with pytest.raises(ValueError, match=match):
+            lora(ad)
+    with pytest.raises(ValueError, match="adapter"):
+        lora(M.LoraExperts(a1=a, b1=b), ids[:3])
+    with pytest.raises(ValueError, match="bias"):
+        M.forward_routing(x, wr, w1, w1, w2, M.Routing(2), torch.zeros(9))
+    with pytest.raises(ValueError, match="CUDA"):
+        M.forward_routing(x, wr, w1, w1, w2, M.Routing(2), torch.zeros(8))
+    with pytest.raises(ValueError, match="scoring"):
+        M.forward_routing(x, wr, w1, w1, w2, M.Routing(2, "relu"))
