@@ -23,9 +23,20 @@ __device__ __forceinline__ float logit_at(const __nv_bfloat16* p) {
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// 2^x to within 2^-22 of the value, and 1 / x to within one ulp (subnormals as 0).
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // sigmoid(l) and 1 - sigmoid(l), each to within a few units of its own last place.
 __device__ __forceinline__ void sigmoid_pair(float l, float& s, float& rest) {
-  const float x = expf(-fabsf(l)), big = __fdividef(1.f, 1.f + x), small = x * big;
+  const float x = expf(-fabsf(l)), big = fast_rcp(1.f + x), small = x * big;
   s = l >= 0.f ? big : small;
   rest = l >= 0.f ? small : big;
 }
@@ -151,17 +162,6 @@ __device__ __forceinline__ unsigned long long ordered(double f) {
   return u ^ ((unsigned long long)((long long)u >> 63) | 0x8000000000000000ull);
 }
 
-// 2^x to within 2^-22 of the value, and 1 / x to within one ulp (subnormals as 0).
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float fast_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Descending, by Batcher's odd-even merge (all indices are known at compile time).
@@ -713,13 +713,13 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
 
 // First pass of the losses: a block's sums of p and of logsumexp^2 and its counts. A lane
 // adds its experts' p over the block's tokens in fp32 (at most a few dozen), the block
-// adds its warps' sums in warp order in double.
+// adds its teams' sums in order in double. Bound by latency: few bytes and few steps per
+// token, so the next token's loads go out before this one's sums.
 template <typename T, int L, int V>
-__global__ void __launch_bounds__(32 * kWarps) k_losses(const Routing r, const T* __restrict__ logits,
-                                                        const int32_t* __restrict__ idx,
-                                                        const uint8_t* __restrict__ mask, int vec,
-                                                        double* __restrict__ part_sum,
-                                                        int32_t* __restrict__ part_count) {
+__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
+    k_losses(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
+             const uint8_t* __restrict__ mask, int vec, double* __restrict__ part_sum,
+             int32_t* __restrict__ part_count) {
   pdl_trigger();
   pdl_wait();
   __shared__ int32_t s_count[513];
@@ -733,23 +733,42 @@ __global__ void __launch_bounds__(32 * kWarps) k_losses(const Routing r, const T
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
   double z = 0.0;
-  for (int64_t t0 = (int64_t)blockIdx.x * kPer; t0 < r.T; t0 += (int64_t)gridDim.x * kPer) {
-    const int64_t t = t0 + threadIdx.x / L;
-    if (t >= r.T || (mask && !mask[t])) continue;
-    const T* row = logits + t * r.stride;
+  int tokens = 0;
+  float ahead[V];
+  int slot = -1;
+  bool keep = false;
+  const auto fetch = [&](int64_t t) {
+    keep = t < r.T;
+    slot = -1;
+    if (!keep) return;
+    load_logits<T, V>(logits + t * r.stride, team.rank, r.E, vec, ahead);
+    if (team.rank < r.k) slot = idx[t * r.k + team.rank];
+    if (mask) keep = mask[t];
+  };
+  int64_t t = (int64_t)blockIdx.x * kPer + threadIdx.x / L;
+  fetch(t);
+  while (t < r.T) {
     float l[V], mx = -INFINITY;
-    load_logits<T, V>(row, team.rank, r.E, vec, l);
 #pragma unroll
-    for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
+    for (int v = 0; v < V; ++v) {
+      l[v] = ahead[v];
+      mx = fmaxf(mx, l[v]);
+    }
+    const bool counts = keep;
+    const int e = slot;
+    t += (int64_t)gridDim.x * kPer;
+    fetch(t);
+    if (!counts) continue;
     mx = team.max(mx);
+    const float top = mx > -INFINITY ? mx : 0.f;  // exp(l - top) is 0 where no expert has a score
     float x[V], sum = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      x[v] = l[v] > -INFINITY ? expf(l[v] - mx) : 0.f;
+      x[v] = expf(l[v] - top);
       sum += x[v];
     }
     sum = team.sum(sum);
-    const float lse = sum > 0.f ? mx + logf(sum) : 0.f;  // no expert has a score: no z term
+    const float lse = sum > 0.f ? top + logf(sum) : 0.f;  // no expert has a score: no z term
     if (r.sigmoid) {
       sum = 0.f;
 #pragma unroll
@@ -762,24 +781,23 @@ __global__ void __launch_bounds__(32 * kWarps) k_losses(const Routing r, const T
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] += x[v] * inv;
-    if (team.rank == 0) {
-      z += (double)lse * (double)lse;
-      atomicAdd(&s_count[r.E], 1);
-    }
-    if (team.rank < r.k) {
-      const int e = idx[t * r.k + team.rank];
-      if (e >= 0 && e < r.E) atomicAdd(&s_count[e], 1);
-    }
+    for (int v = 0; v < V; ++v) acc[v] = fmaf(x[v], inv, acc[v]);
+    z += (double)lse * (double)lse;
+    ++tokens;
+    if (e >= 0 && e < r.E) atomicAdd(&s_count[e], 1);
   }
   const int who = threadIdx.x / L;
 #pragma unroll
   for (int v = 0; v < V; ++v) s_sum[who][team.rank * V + v] = acc[v];
-  if (team.rank == 0) s_z[who] = z;
+  if (team.rank == 0) {
+    s_z[who] = z;
+    atomicAdd(&s_count[r.E], tokens);
+  }
   __syncthreads();
   const int64_t out = (int64_t)blockIdx.x * (r.E + 1);
   for (int e = threadIdx.x; e <= r.E; e += blockDim.x) {
     double sum = 0.0;
+#pragma unroll 8
     for (int w = 0; w < kPer; ++w) sum += e < r.E ? (double)s_sum[w][e] : s_z[w];
     part_sum[out + e] = sum;
     part_count[out + e] = s_count[e];
@@ -787,7 +805,8 @@ __global__ void __launch_bounds__(32 * kWarps) k_losses(const Routing r, const T
 }
 
 // Second pass, one block: thread (e, part) adds every nparts-th block's partials, then
-// the parts are added in order, and one warp's worth of threads the experts.
+// the parts are added in order, and one warp's worth of threads the experts. Loads go out
+// eight at a time: with one block there is nothing else to wait beside.
 __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks,
                                                      const double* __restrict__ part_sum,
                                                      const int32_t* __restrict__ part_count,
@@ -805,33 +824,43 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
   double sum = 0.0;
   int32_t count = 0;
   if (part < nparts) {
-    for (int b = part; b < blocks; b += nparts) {
-      sum += part_sum[(int64_t)b * n + e];
-      count += part_count[(int64_t)b * n + e];
+    for (int b = part; b < blocks; b += 8 * nparts) {
+      double s[8];
+      int32_t c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = b + i * nparts;
+        s[i] = at < blocks ? part_sum[(int64_t)at * n + e] : 0.0;
+        c[i] = at < blocks ? part_count[(int64_t)at * n + e] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum += s[i];
+        count += c[i];
+      }
     }
   }
   s_sum[threadIdx.x] = sum;
   s_count[threadIdx.x] = count;
   __syncthreads();
-  if (threadIdx.x < n) {
-    for (int p = 1; p < nparts; ++p) {
-      sum += s_sum[p * n + threadIdx.x];
-      count += s_count[p * n + threadIdx.x];
+  // the parts in pairs, log2 steps
+  int live = nparts;
+  while (live > 1) {
+    const int half = (live + 1) / 2;
+    if (part < live - half) {
+      s_sum[threadIdx.x] += s_sum[threadIdx.x + half * n];
+      s_count[threadIdx.x] += s_count[threadIdx.x + half * n];
     }
-    counts[threadIdx.x] = count;
+    live = half;
+    __syncthreads();
   }
-  __syncthreads();
-  if (threadIdx.x < n) {
-    s_sum[threadIdx.x] = sum;
-    s_count[threadIdx.x] = count;
-  }
-  __syncthreads();
   const double tokens = s_count[r.E] > 0 ? (double)s_count[r.E] : 1.0;
   double bal = 0.0;
+  if (threadIdx.x < n) counts[threadIdx.x] = s_count[threadIdx.x];
   if (threadIdx.x < r.E) {
-    const double mean = sum / tokens;
+    const double mean = s_sum[threadIdx.x] / tokens;
     prob_mean[threadIdx.x] = (float)mean;
-    bal = (double)count / tokens * mean;
+    bal = (double)s_count[threadIdx.x] / tokens * mean;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) bal += __shfl_xor_sync(0xffffffffu, bal, o);
@@ -839,7 +868,7 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
   __syncthreads();
   if (threadIdx.x == 0) {
     double all = 0.0;
-    for (int w = 0; w < 32; ++w) all += s_bal[w];
+    for (int w = 0; w < (r.E + 31) / 32; ++w) all += s_bal[w];
     losses[0] = (float)(all * r.E);
     losses[1] = (float)(s_sum[r.E] / tokens);
   }
@@ -855,7 +884,7 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
 //   balance: softmax p_e (c_e - sum c p); sigmoid s_e (1 - s_e) (c_e - sum c p) / sum s;
 //   z: 2 d1 / N * logsumexp * softmax_e.
 template <typename T, int L, int V>
-__global__ void __launch_bounds__(32 * kWarps)
+__global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
     k_route_bwd(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
                 const float* __restrict__ d_w, const int32_t* __restrict__ counts,
                 const float* __restrict__ d_losses, const uint8_t* __restrict__ mask, int vec,
@@ -866,6 +895,17 @@ __global__ void __launch_bounds__(32 * kWarps)
   constexpr int kPer = 32 / L * kWarps;
   __shared__ __align__(16) float s_slots[kWarps * 32 / L][L * V];
   float* slots = s_slots[threadIdx.x / L];
+  int pairs = 1;  // lanes up to the next power of two of k
+  while (pairs < r.k) pairs *= 2;
+  // over the slots' lanes (the others get what theirs amount to)
+  const auto slots_sum = [&](float v) {
+    for (int o = pairs >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(team.mask, v, o);
+    return v;
+  };
+  const auto slots_max = [&](float v) {
+    for (int o = pairs >> 1; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(team.mask, v, o));
+    return v;
+  };
   float c[V], zc = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) c[v] = 0.f;
@@ -903,15 +943,16 @@ __global__ void __launch_bounds__(32 * kWarps)
     const bool need_p = losses || (d_w && !r.sigmoid && !r.renorm);
     if (need_p) {
       mx = team.max(mx);
+      const float top = mx > -INFINITY ? mx : 0.f;  // exp(l - top) is 0 where no expert has a score
       float sum = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        p[v] = l[v] > -INFINITY ? expf(l[v] - mx) : 0.f;
+        p[v] = expf(l[v] - top);
         sum += p[v];
       }
       sum = team.sum(sum);
-      lse = sum > 0.f ? mx + logf(sum) : 0.f;
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      lse = sum > 0.f ? top + logf(sum) : 0.f;
+      const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) p[v] *= inv;
     }
@@ -930,11 +971,11 @@ __global__ void __launch_bounds__(32 * kWarps)
           dl[v] = s[v] * rest;
         }
         sum = team.sum(sum);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
         cs = team.sum(cs) * inv;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          dl[v] = dl[v] * (c[v] - cs) * inv + zc * lse * p[v];
+          dl[v] = dl[v] * ((c[v] - cs) * inv) + zc * lse * p[v];
         }
       } else {
 #pragma unroll
@@ -949,33 +990,47 @@ __global__ void __launch_bounds__(32 * kWarps)
       if (r.sigmoid) {
         if (my_e >= 0) sigmoid_pair(ls, u, rest);
       } else if (r.renorm) {
-        const float top = team.max(ls);
+        const float top = slots_max(ls);
         if (ls > -INFINITY) u = expf(ls - top);
       }
       float term = 0.f;  // what slot `rank` adds to its expert
       if (r.renorm) {
-        const float sum = team.sum(u);
-        u = sum > 0.f ? u / sum : 0.f;
-        term = u * (g - team.sum(g * u)) * rest;
+        const float sum = slots_sum(u);
+        u = sum > 0.f ? __fdividef(u, sum) : 0.f;
+        term = u * (g - slots_sum(g * u)) * rest;
       } else if (r.sigmoid) {
         term = u * rest * g;
       } else {
         float gp = 0.f;
         if (my_e >= 0 && ls > -INFINITY) u = expf(ls - lse);
-        gp = team.sum(g * u);
+        gp = team.sum(g * u);  // every lane needs it
         term = u * g;
 #pragma unroll
         for (int v = 0; v < V; ++v) dl[v] -= p[v] * gp;
       }
       // from the slots' lanes to their experts'
       __syncwarp(team.mask);
+      if constexpr (V % 4 == 0) {
+        float4* own = reinterpret_cast<float4*>(slots + team.rank * V);
 #pragma unroll
-      for (int v = 0; v < V; ++v) slots[team.rank * V + v] = 0.f;
-      __syncwarp(team.mask);
-      if (my_e >= 0) atomicAdd(slots + my_e, term);
-      __syncwarp(team.mask);
+        for (int v = 0; v < V / 4; ++v) own[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncwarp(team.mask);
+        if (my_e >= 0) atomicAdd(slots + my_e, term);
+        __syncwarp(team.mask);
 #pragma unroll
-      for (int v = 0; v < V; ++v) dl[v] += slots[team.rank * V + v];
+        for (int v = 0; v < V / 4; ++v) {
+          const float4 f = own[v];
+          dl[4 * v] += f.x, dl[4 * v + 1] += f.y, dl[4 * v + 2] += f.z, dl[4 * v + 3] += f.w;
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) slots[team.rank * V + v] = 0.f;
+        __syncwarp(team.mask);
+        if (my_e >= 0) atomicAdd(slots + my_e, term);
+        __syncwarp(team.mask);
+#pragma unroll
+        for (int v = 0; v < V; ++v) dl[v] += slots[team.rank * V + v];
+      }
     }
     store_row<T, V>(d_logits + t * r.E, team.rank, r.E, vec_out, dl);
   }
@@ -1060,8 +1115,8 @@ cudaError_t launch_route(const Routing& r, const void* logits, const float* bias
 
 int router_loss_blocks(const Routing& r) {
   int n = 0;
-  by_sizes(r, [&](auto l, auto) {
-    n = (int)token_blocks<decltype(l)::value>(r, 2);
+  by_sizes(r, [&](auto l, auto v) {
+    n = (int)token_blocks<decltype(l)::value>(r, decltype(v)::value <= 8 ? 3 : 2);
     return cudaSuccess;
   });
   return n;
@@ -1096,7 +1151,7 @@ cudaError_t launch_route_backward(const Routing& r, const void* logits, const in
                                   const uint8_t* mask, void* d_logits, cudaStream_t st) {
   return by_sizes(r, [&](auto l, auto v) {
     constexpr int L = decltype(l)::value, V = decltype(v)::value;
-    const dim3 grid(token_blocks<L>(r, 8)), block(32 * kWarps);
+    const dim3 grid(token_blocks<L>(r, V <= 4 ? 6 : V <= 8 ? 4 : 2)), block(32 * kWarps);
     if (r.bf16) {
       const auto* p = static_cast<const __nv_bfloat16*>(logits);
       return launch_pdl(k_route_bwd<__nv_bfloat16, L, V>, grid, block, 0, st, r, p, idx, d_w, counts,
