@@ -1049,7 +1049,9 @@ cudaError_t with(F f) {
   return f(std::integral_constant<int, L>(), std::integral_constant<int, V>());
 }
 
-// Routing: a lane per slot, and one per group at least; up to 8 slots by the merge.
+// Routing: a lane per slot, and one per group at least; up to 8 slots by the merge. Few tokens
+// leave the SMs idle, so their teams are wider: shorter chains, and room for near ties beside
+// 8 slots (250 x 64 with a bias 9.5 -> 5.2 us, 1024 x 256 6.1 -> 5.7; but 65536 x 64 22 -> 35).
 template <typename F>
 cudaError_t by_choice(const Routing& r, F f) {
   const auto few = [&](auto l, auto v) { return f(l, v, std::true_type()); };
@@ -1058,9 +1060,10 @@ cudaError_t by_choice(const Routing& r, F f) {
     if (r.E <= 8) return with<8, 1>(few);
     if (r.E <= 16) return with<8, 2>(few);
     if (r.E <= 32) return with<8, 4>(few);
-    if (r.E <= 64) return with<8, 8>(few);
-    if (r.E <= 128) return with<8, 16>(few);
-    if (r.E <= 256) return with<16, 16>(few);
+    const bool wide = r.T <= 4096;
+    if (r.E <= 64) return wide ? with<16, 4>(few) : with<8, 8>(few);
+    if (r.E <= 128) return wide ? with<16, 8>(few) : with<8, 16>(few);
+    if (r.E <= 256) return wide ? with<32, 8>(few) : with<16, 16>(few);
     return with<32, 16>(few);
   }
   if (r.E <= 64) return with<32, 2>(many);
