@@ -512,7 +512,8 @@ moe_status_t moe_forward_routing(const moe_shape_t* shape, const moe_routing_t* 
  *   outside [0, E) names no expert); token_mask [T] uint8, nullable (all tokens count);
  *   losses [2] fp32 out; counts [E + 1] int32 out, counts[E] = N; prob_mean [E] fp32 out
  *   (P); ws a device workspace of moe_router_losses_workspace() bytes (256-byte aligned;
- *   its content does not matter). Uses only num_experts, num_experts_per_tok, scoring,
+ *   its content does not matter; 0 where none is needed, for few tokens, ws may then be NULL,
+ *   and where the arguments are invalid, moe_last_error() then says why). Uses only num_experts, num_experts_per_tok, scoring,
  *   num_tokens and the logits fields of `routing`. */
 size_t moe_router_losses_workspace(const moe_routing_t* routing);
 moe_status_t moe_router_losses(const moe_routing_t* routing, const void* logits,

@@ -189,7 +189,8 @@ struct Routing {
 cudaError_t launch_route(const Routing& r, const void* logits, const float* bias, int32_t* idx,
                          float* w, cudaStream_t st);
 
-// Blocks of the losses' first pass: each leaves E + 1 partial sums and E + 1 counts.
+// Blocks of the losses' first pass: each leaves E + 1 partial sums and E + 1 counts. 0: the
+// tokens are few enough for one launch without scratch.
 int router_loss_blocks(const Routing& r);
 cudaError_t launch_router_losses(const Routing& r, const void* logits, const int32_t* idx,
                                  const uint8_t* mask, float* losses, int32_t* counts,
@@ -278,6 +279,33 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// launch_pdl with a cluster of `cluster` neighbouring blocks.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem,
+                           unsigned cluster, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// All blocks of the cluster arrive, and see each other's writes to shared memory.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 }  // namespace moe

@@ -713,20 +713,18 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
 
 // First pass of the losses: a block's sums of p and of logsumexp^2 and its counts. A lane
 // adds its experts' p over the block's tokens in fp32 (at most a few dozen), the block
-// adds its teams' sums in order in double. Bound by latency: few bytes and few steps per
+// adds its teams' sums in order in double: E + 1 sums and counts. Bound by latency: few bytes and few steps per
 // token, so the next token's loads go out before this one's sums.
-template <typename T, int L, int V>
-__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
-    k_losses(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
-             const uint8_t* __restrict__ mask, int vec, double* __restrict__ part_sum,
-             int32_t* __restrict__ part_count) {
-  pdl_trigger();
-  pdl_wait();
+template <typename T, int L, int V, int WARPS>
+__device__ __forceinline__ void block_losses(const Routing& r, const T* __restrict__ logits,
+                                             const int32_t* __restrict__ idx,
+                                             const uint8_t* __restrict__ mask, int vec,
+                                             double* part_sum, int32_t* part_count) {
   __shared__ int32_t s_count[513];
-  __shared__ float s_sum[kWarps * 32 / L][L * V];
-  __shared__ double s_z[kWarps * 32 / L];
+  __shared__ float s_sum[WARPS * 32 / L][L * V];
+  __shared__ double s_z[WARPS * 32 / L];
   const Team<L> team;
-  constexpr int kPer = 32 / L * kWarps;
+  constexpr int kPer = 32 / L * WARPS;
   for (int e = threadIdx.x; e <= r.E; e += blockDim.x) s_count[e] = 0;
   __syncthreads();
   float acc[V];
@@ -794,14 +792,98 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
     atomicAdd(&s_count[r.E], tokens);
   }
   __syncthreads();
-  const int64_t out = (int64_t)blockIdx.x * (r.E + 1);
   for (int e = threadIdx.x; e <= r.E; e += blockDim.x) {
     double sum = 0.0;
 #pragma unroll 8
     for (int w = 0; w < kPer; ++w) sum += e < r.E ? (double)s_sum[w][e] : s_z[w];
-    part_sum[out + e] = sum;
-    part_count[out + e] = s_count[e];
+    part_sum[e] = sum;
+    part_count[e] = s_count[e];
   }
+}
+
+template <typename T, int L, int V>
+__global__ void __launch_bounds__(32 * kWarps, V <= 8 ? 3 : 2)
+    k_losses(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
+             const uint8_t* __restrict__ mask, int vec, double* __restrict__ part_sum,
+             int32_t* __restrict__ part_count) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t out = (int64_t)blockIdx.x * (r.E + 1);
+  block_losses<T, L, V, kWarps>(r, logits, idx, mask, vec, part_sum + out, part_count + out);
+}
+
+// The losses from the sums over all tokens, by one block of 1024 threads: thread e <= E holds
+// expert e's sum of p (e = E: the sum of logsumexp^2) and count (e = E: the tokens).
+__device__ __forceinline__ void finish_losses(const Routing& r, double sum, int32_t count,
+                                              float* __restrict__ losses, int32_t* __restrict__ counts,
+                                              float* __restrict__ prob_mean) {
+  __shared__ double s_bal[32], s_z;
+  __shared__ int32_t s_tokens;
+  const int e = threadIdx.x;
+  if (e == r.E) {
+    s_z = sum;
+    s_tokens = count;
+  }
+  __syncthreads();
+  const double tokens = s_tokens > 0 ? (double)s_tokens : 1.0;
+  double bal = 0.0;
+  if (e <= r.E) counts[e] = count;
+  if (e < r.E) {
+    const double mean = sum / tokens;
+    prob_mean[e] = (float)mean;
+    bal = (double)count / tokens * mean;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) bal += __shfl_xor_sync(0xffffffffu, bal, o);
+  if ((e & 31) == 0) s_bal[e >> 5] = bal;
+  __syncthreads();
+  if (e == 0) {
+    double all = 0.0;
+    for (int w = 0; w < (r.E + 31) / 32; ++w) all += s_bal[w];
+    losses[0] = (float)(all * r.E);
+    losses[1] = (float)(s_z / tokens);
+  }
+}
+
+// Few tokens: one launch, a cluster of 8 blocks of 1024 threads whose first block adds the
+// sums up from their shared memory, in order; no workspace. For 4096 x 8 a call takes 19 us with
+// the two passes, most of it launches and allocations.
+constexpr int kLossCluster = 8;
+constexpr int64_t kLossTokens = 8192;
+
+template <typename T, int L, int V>
+__global__ void __launch_bounds__(1024)
+    k_losses_few(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
+                 const uint8_t* __restrict__ mask, int vec, float* __restrict__ losses,
+                 int32_t* __restrict__ counts, float* __restrict__ prob_mean) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ double s_part[L * V + 1];
+  __shared__ int32_t s_parts[L * V + 1];
+  block_losses<T, L, V, 32>(r, logits, idx, mask, vec, s_part, s_parts);
+  cluster_sync();
+  if (blockIdx.x == 0) {
+    double sum = 0.0;
+    int32_t count = 0;
+    if ((int)threadIdx.x <= r.E) {
+      const uint32_t a = (uint32_t)__cvta_generic_to_shared(&s_part[threadIdx.x]);
+      const uint32_t b = (uint32_t)__cvta_generic_to_shared(&s_parts[threadIdx.x]);
+#pragma unroll
+      for (int w = 0; w < kLossCluster; ++w) {
+        uint32_t there;
+        double s;
+        int32_t c;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(a), "r"(w));
+        asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(s) : "r"(there) : "memory");
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(b), "r"(w));
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(there) : "memory");
+        sum += s;
+        count += c;
+      }
+    }
+    finish_losses(r, sum, count, losses, counts, prob_mean);
+  }
+  cluster_sync();  // no block leaves while the first reads its sums
 }
 
 // Second pass, one block: thread (e, part) adds every nparts-th block's partials, then
@@ -817,7 +899,6 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
   pdl_wait();
   __shared__ double s_sum[1024];
   __shared__ int32_t s_count[1024];
-  __shared__ double s_bal[32];
   const int n = r.E + 1;
   const int nparts = 1024 / n;
   const int part = threadIdx.x / n, e = threadIdx.x - part * n;
@@ -854,24 +935,8 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
     live = half;
     __syncthreads();
   }
-  const double tokens = s_count[r.E] > 0 ? (double)s_count[r.E] : 1.0;
-  double bal = 0.0;
-  if (threadIdx.x < n) counts[threadIdx.x] = s_count[threadIdx.x];
-  if (threadIdx.x < r.E) {
-    const double mean = s_sum[threadIdx.x] / tokens;
-    prob_mean[threadIdx.x] = (float)mean;
-    bal = (double)s_count[threadIdx.x] / tokens * mean;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) bal += __shfl_xor_sync(0xffffffffu, bal, o);
-  if ((threadIdx.x & 31) == 0) s_bal[threadIdx.x >> 5] = bal;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double all = 0.0;
-    for (int w = 0; w < (r.E + 31) / 32; ++w) all += s_bal[w];
-    losses[0] = (float)(all * r.E);
-    losses[1] = (float)(s_sum[r.E] / tokens);
-  }
+  const bool mine = threadIdx.x < n;
+  finish_losses(r, mine ? s_sum[threadIdx.x] : 0.0, mine ? s_count[threadIdx.x] : 0, losses, counts, prob_mean);
 }
 
 // Gradient in the logits. With g_j = weight_scale * d_topk_w[j], and for the losses
@@ -1116,7 +1181,12 @@ cudaError_t launch_route(const Routing& r, const void* logits, const float* bias
   });
 }
 
+namespace {
+bool few_for_losses(const Routing& r) { return r.T <= kLossTokens && r.E <= 256; }
+}  // namespace
+
 int router_loss_blocks(const Routing& r) {
+  if (few_for_losses(r)) return 0;
   int n = 0;
   by_sizes(r, [&](auto l, auto v) {
     n = (int)token_blocks<decltype(l)::value>(r, decltype(v)::value <= 8 ? 3 : 2);
@@ -1129,6 +1199,23 @@ cudaError_t launch_router_losses(const Routing& r, const void* logits, const int
                                  const uint8_t* mask, float* losses, int32_t* counts,
                                  float* prob_mean, double* part_sum, int32_t* part_count,
                                  cudaStream_t st) {
+  if (few_for_losses(r))
+    return by_sizes(r, [&](auto l, auto v) {
+      constexpr int L = decltype(l)::value, V = decltype(v)::value;
+      if constexpr (V > 8) {
+        return cudaErrorInvalidValue;  // not reached: E <= 256
+      } else {
+        if (r.bf16) {
+          const auto* p = static_cast<const __nv_bfloat16*>(logits);
+          return launch_cluster(k_losses_few<__nv_bfloat16, L, V>, kLossCluster, 1024, 0, kLossCluster,
+                                st, r, p, idx, mask, vectors<__nv_bfloat16, V>(r, p, r.stride), losses,
+                                counts, prob_mean);
+        }
+        const auto* p = static_cast<const float*>(logits);
+        return launch_cluster(k_losses_few<float, L, V>, kLossCluster, 1024, 0, kLossCluster, st, r, p,
+                              idx, mask, vectors<float, V>(r, p, r.stride), losses, counts, prob_mean);
+      }
+    });
   const int blocks = router_loss_blocks(r);
   if (blocks > 0) {
     const cudaError_t e = by_sizes(r, [&](auto l, auto v) {

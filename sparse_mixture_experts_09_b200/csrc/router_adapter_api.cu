@@ -111,7 +111,7 @@ LossLayout loss_layout(const Routing& r) {
   const size_t n = (size_t)router_loss_blocks(r) * (r.E + 1);
   LossLayout l;
   l.count = (n * 8 + 255) / 256 * 256;
-  l.end = l.count + (n * 4 + 255) / 256 * 256 + 256;
+  l.end = l.count + (n * 4 + 255) / 256 * 256;
   return l;
 }
 
@@ -186,7 +186,7 @@ moe_status_t moe_router_losses(const moe_routing_t* routing, const void* logits,
   MOE_TRY(check_aligned(counts, "counts", 4, false));
   MOE_TRY(check_aligned(prob_mean, "prob_mean", 4, false));
   const LossLayout l = loss_layout(r);
-  if (!ws || reinterpret_cast<uintptr_t>(ws) % 256)
+  if (l.end && (!ws || reinterpret_cast<uintptr_t>(ws) % 256))
     return fail_with(MOE_ERR_WORKSPACE, "workspace is NULL or not 256-byte aligned");
   if (ws_bytes < l.end)
     return fail_with(MOE_ERR_WORKSPACE, "workspace too small: need %zu bytes, got %zu", l.end,

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from functools import lru_cache
 from typing import NamedTuple, Optional
 
 import torch
@@ -828,22 +829,26 @@ _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
 _LOGITS = (torch.float32, torch.bfloat16)
 
 
+@lru_cache(maxsize=256)
+def _routing_struct(routing: Routing, t: int, stride: int, e: int, bf16: bool) -> _RoutingArgs:
+    if routing.scoring not in _SCORING:
+        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {routing.scoring!r}")
+    return _RoutingArgs(t, stride, e, routing.k, _SCORING[routing.scoring], routing.num_groups,
+                        routing.topk_groups, routing.group_top, int(routing.renormalize), int(bf16),
+                        routing.scale)
+
+
 def _routing_args(logits, routing: Routing) -> _RoutingArgs:
     if logits.dim() != 2:
         raise ValueError(f"logits must be [tokens, experts], got {tuple(logits.shape)}")
     t, e = logits.shape
     if logits.dtype not in _LOGITS:
         raise ValueError(f"logits must be torch.float32 or torch.bfloat16, got {logits.dtype}")
-    if routing.scoring not in _SCORING:
-        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {routing.scoring!r}")
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor")
     if e > 1 and logits.stride(1) != 1:
         raise ValueError("logits must be contiguous along the experts")
-    stride = logits.stride(0) if t > 1 else e
-    return _RoutingArgs(t, stride, e, routing.k, _SCORING[routing.scoring], routing.num_groups,
-                        routing.topk_groups, routing.group_top, int(routing.renormalize),
-                        int(logits.dtype == torch.bfloat16), routing.scale)
+    return _routing_struct(routing, t, logits.stride(0) if t > 1 else e, e, logits.dtype is torch.bfloat16)
 
 
 def route(logits, routing: Routing, bias=None, stream=None):
@@ -872,11 +877,7 @@ def forward_routing(x, w_router, w1, w3, w2, routing: Routing, bias=None, residu
     t, h = x.shape
     e, i, _ = w1.shape
     shape = make_shape(t, h, i, e, routing.k, weight_layout, router_bf16_logits)
-    if routing.scoring not in _SCORING:
-        raise ValueError(f"scoring must be 'softmax' or 'sigmoid', got {routing.scoring!r}")
-    args = _RoutingArgs(t, e, e, routing.k, _SCORING[routing.scoring], routing.num_groups,
-                        routing.topk_groups, routing.group_top, int(routing.renormalize), 0,
-                        routing.scale)
+    args = _routing_struct(routing, t, e, e, False)
     _layer_sizes(t, h, e, i, w_router, logit_bias, residual, out, bias=(bias, e),
                  **_bf16_weights(e, i, h, w1, w3, w2))
     xp = _dev(x, "x", torch.bfloat16)
@@ -910,13 +911,14 @@ def router_losses(logits, topk_idx, routing: Routing, token_mask=None, stream=No
     mask = _token_mask(token_mask, t, dev)
 
     def call(st):
-        n = lib().moe_router_losses_workspace(args)
-        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        n = lib().moe_router_losses_workspace(args)    # 0: few tokens need none
+        ws = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
         losses = torch.empty(2, dtype=torch.float32, device=dev)
         counts = torch.empty(e + 1, dtype=torch.int32, device=dev)
         prob = torch.empty(e, dtype=torch.float32, device=dev)
         _check(lib().moe_router_losses(args, logits.data_ptr(), idx, mask, losses.data_ptr(),
-                                       counts.data_ptr(), prob.data_ptr(), ws.data_ptr(), n, st))
+                                       counts.data_ptr(), prob.data_ptr(),
+                                       None if ws is None else ws.data_ptr(), n, st))
         return RouterLosses(losses, counts, prob)
 
     return _on(dev, stream, call)

@@ -167,7 +167,7 @@ def _range(l, floor=30.0):
     return floor if np.isinf(l).any() else min(floor, float((l.max(1, keepdims=True) - l).max()))
 
 
-@pytest.mark.parametrize("t,e,k", SHAPES + [(20011, 8, 2), (5000, 64, 6)])
+@pytest.mark.parametrize("t,e,k", SHAPES + [(20011, 8, 2), (5000, 64, 6), (8192, 16, 2), (8193, 8, 2), (7777, 256, 8)])
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_losses(t, e, k, scoring):
     for kind in ("normal", "special"):

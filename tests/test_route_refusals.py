@@ -47,13 +47,15 @@ def test_bad_pointers_are_refused(L):
     for call in ((None, None, 16, 16), (18, None, 16, 16), (16, 6, 16, 16), (16, None, None, 16), (16, None, 16, 2)):
         assert L.moe_route(args(), *call, None) == 1
         assert L.moe_last_error()
-    need = L.moe_router_losses_workspace(args())
+    assert L.moe_router_losses_workspace(args()) == 0 and not L.moe_last_error()   # few tokens need none
+    many = args(num_tokens=100000)
+    need = L.moe_router_losses_workspace(many)
     assert need > 0
-    assert L.moe_router_losses(args(), 16, 16, None, 16, 16, 16, 256, need - 1, None) == 3
-    assert L.moe_router_losses(args(), 16, 16, None, 16, 16, 16, 128, need, None) == 3
-    assert L.moe_router_losses(args(), 16, 16, None, 16, 16, 16, None, need, None) == 3
-    assert L.moe_router_losses(args(), 16, None, None, 16, 16, 16, 256, need, None) == 1
-    assert L.moe_router_losses(args(), 16, 16, None, None, 16, 16, 256, need, None) == 1
+    assert L.moe_router_losses(many, 16, 16, None, 16, 16, 16, 256, need - 1, None) == 3
+    assert L.moe_router_losses(many, 16, 16, None, 16, 16, 16, 128, need, None) == 3
+    assert L.moe_router_losses(many, 16, 16, None, 16, 16, 16, None, need, None) == 3
+    assert L.moe_router_losses(many, 16, None, None, 16, 16, 16, 256, need, None) == 1
+    assert L.moe_router_losses(args(), 16, 16, None, None, 16, 16, None, 0, None) == 1
     assert L.moe_route_backward(args(), 16, 16, 16, 16, None, None, 16, None) == 1
     assert b"go together" in L.moe_last_error()
     assert L.moe_route_backward(args(), 16, 16, 16, None, 16, None, 16, None) == 1
@@ -72,7 +74,7 @@ def test_binding_refuses(L):
     l = torch.zeros(4, 8)
     idx = torch.zeros(4, 2, dtype=torch.int32)
     for call, match in ((lambda: M.route(l, r), "CUDA"), (lambda: M.route(torch.zeros(8), r), "tokens, experts"),
-                        (lambda: M.route(l.double(), r), "float32"), (lambda: M.route(l, M.Routing(2, "tanh")), "scoring"),
+                        (lambda: M.route(l.double(), r), "float32"), (lambda: M._routing_struct(M.Routing(2, "tanh"), 4, 8, 8, False), "scoring"),
                         (lambda: M.router_losses(l, idx, r), "CUDA"), (lambda: M.route_backward(l, idx, r), "CUDA")):
         with pytest.raises(ValueError, match=match):
             call()
