@@ -67,19 +67,6 @@ struct Team {
     for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(mask, v, o));
     return v;
   }
-  __device__ double max(double v) const {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(mask, v, o));
-    return v;
-  }
-  __device__ unsigned long long max(unsigned long long v) const {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) {
-      const unsigned long long w = __shfl_xor_sync(mask, v, o);
-      v = w > v ? w : v;
-    }
-    return v;
-  }
   template <typename T>
   __device__ T from(T v, int r) const {
     return __shfl_sync(mask, v, base + r);
@@ -156,12 +143,6 @@ __device__ __forceinline__ void store_row(T* row, int rank, int E, bool vec, con
   }
 }
 
-// Doubles as unsigned numbers of the same order (-0 as +0); all are above 0.
-__device__ __forceinline__ unsigned long long ordered(double f) {
-  const unsigned long long u = (unsigned long long)__double_as_longlong(f + 0.0);
-  return u ^ ((unsigned long long)((long long)u >> 63) | 0x8000000000000000ull);
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Descending, by Batcher's odd-even merge (all indices are known at compile time).
@@ -209,84 +190,52 @@ struct Groups {
   }
 };
 
-// The groups that stay, as a ballot (bit base + g * lanes for group g). With CHECK a value may
-// be off by tol + 2 u |value|; `close` is set where the last group that stays and the first
-// that goes are not further apart than that allows.
-// A group's one or two best: its lanes take their own values, or every lanes-th from shared
-// memory, and merge their pairs; group_top > 2 takes the largest left group_top times.
-template <bool CHECK, typename K, int L, int V>
+// The groups that stay, as a ballot (bit base + g * lanes for group g). A value may be off by
+// tol + 2 u |value|; `close` is set where the last group that stays and the first that goes
+// are not further apart than that allows. A group's one or two best: its lanes take their own
+// values, or every lanes-th from shared memory, and merge their pairs.
+template <int L, int V>
 __device__ __forceinline__ unsigned open_groups(const Routing& r, const Team<L>& team,
-                                                const Groups<L, V>& groups, const K (&value)[V], K tol,
-                                                K* shared, bool& close) {
+                                                const Groups<L, V>& groups, const float (&value)[V],
+                                                float tol, float* shared, bool& close) {
   const int lanes = groups.lanes, g = team.rank / lanes;
-  const K none = -INFINITY;
   const auto at_expert = [](int e) { return e + (e >> 5); };  // groups of 32 on distinct banks
-  const bool own = CHECK && groups.size == V * lanes;  // the lanes hold their group's values
+  const bool own = groups.size == V * lanes;  // the lanes hold their group's values
   if (!own) {
     __syncwarp(team.mask);
 #pragma unroll
     for (int v = 0; v < V; ++v) shared[at_expert(team.rank * V + v)] = value[v];
     __syncwarp(team.mask);
   }
-  K m1 = none, m2 = none;
-  if (CHECK || r.group_top <= 2) {
-    const auto add = [&](K x) {
-      const K low = x < m1 ? x : m1;
-      m2 = low > m2 ? low : m2;
-      m1 = x > m1 ? x : m1;
-    };
-    if (own) {
+  float m1 = -INFINITY, m2 = -INFINITY;
+  const auto add = [&](float x) {
+    m2 = fmaxf(m2, fminf(x, m1));
+    m1 = fmaxf(m1, x);
+  };
+  if (own) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) add(value[v]);
-    } else if (g < r.groups) {
-      for (int i = team.rank - g * lanes; i < groups.size; i += lanes)
-        add(shared[at_expert(g * groups.size + i)]);
-    }
-    for (int o = lanes >> 1; o > 0; o >>= 1) {
-      const K o1 = __shfl_xor_sync(team.mask, m1, o), o2 = __shfl_xor_sync(team.mask, m2, o);
-      const K low = o1 < m1 ? o1 : m1;
-      m2 = o2 > m2 ? o2 : m2;
-      m2 = low > m2 ? low : m2;
-      m1 = o1 > m1 ? o1 : m1;
-    }
-  } else {
-    m1 = 0;
-    for (int n = 0; n < r.group_top; ++n) {
-      K best = none;
-      int at = 0x7fffffff;
-      if (g < r.groups)
-        for (int i = team.rank - g * lanes; i < groups.size; i += lanes) {
-          const K x = shared[at_expert(g * groups.size + i)];
-          if (x > best || (x == best && i < at && x > none)) {
-            best = x;
-            at = i;
-          }
-        }
-      for (int o = lanes >> 1; o > 0; o >>= 1) {
-        const K ob = __shfl_xor_sync(team.mask, best, o);
-        const int oa = __shfl_xor_sync(team.mask, at, o);
-        if (ob > best || (ob == best && oa < at)) {
-          best = ob;
-          at = oa;
-        }
-      }
-      m1 += best;
-      if (at != 0x7fffffff && at % lanes == team.rank - g * lanes) shared[at_expert(g * groups.size + at)] = none;
-    }
+    for (int v = 0; v < V; ++v) add(value[v]);
+  } else if (g < r.groups) {
+    for (int i = team.rank - g * lanes; i < groups.size; i += lanes)
+      add(shared[at_expert(g * groups.size + i)]);
   }
-  const K mine = r.group_top == 2 ? m1 + m2 : m1;
+  for (int o = lanes >> 1; o > 0; o >>= 1) {
+    const float o1 = __shfl_xor_sync(team.mask, m1, o), o2 = __shfl_xor_sync(team.mask, m2, o);
+    m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+    m1 = fmaxf(m1, o1);
+  }
+  const float mine = r.group_top == 2 ? m1 + m2 : m1;
   int above = 0;
   for (int j = 0; j < r.groups; ++j) {
-    const K other = team.from(mine, j * lanes);
+    const float other = team.from(mine, j * lanes);
     above += other > mine || (other == mine && j < g);
   }
   const bool in = above < r.topk_groups;
-  if (CHECK) {
-    const bool real = g < r.groups;
-    const K off = real ? 2 * tol + (K)0x1p-22 * (fabs(m1) + (r.group_top == 2 ? fabs(m2) : (K)0)) : (K)0;
-    const K least = -team.max(real && in ? -mine : none), most = team.max(real && !in ? mine : none);
-    close = r.topk_groups < r.groups && !(least - most > 2 * team.max(off));
-  }
+  const bool real = g < r.groups;
+  // what a group's value may be off by: its terms' bounds and their sum's rounding
+  const float off = real ? 2 * tol + 0x1p-22f * (fabsf(m1) + (r.group_top == 2 ? fabsf(m2) : 0.f)) : 0.f;
+  const float least = -team.max(real && in ? -mine : -INFINITY), most = team.max(real && !in ? mine : -INFINITY);
+  close = r.topk_groups < r.groups && !(least - most > 2 * team.max(off));
   return __ballot_sync(team.mask, in);
 }
 
@@ -351,16 +300,16 @@ __device__ __forceinline__ int best_experts(const Routing& r, const Team<L>& tea
 
 // As best_experts for k <= 8, without its k rounds in a row: the lanes' sorted lists, cut to 8,
 // are merged in log2 L steps (of two descending lists the larger of each pair a[i], b[7 - i] is
-// the best 8, and three exchange stages sort them), the k-th value marks the candidates, a
-// prefix sum gives each a lane, and a candidate's slot is the number of those above it.
-// Returns the lane's candidate; slot < k where it is chosen. `unsure` (a team's lanes agree): the
-// choice is not to be had this way.
+// the best 8, and three exchange stages sort them), the k-th value marks the candidates, and a
+// prefix sum gives each a lane: n of them, in the order of their indices. Returns the lane's
+// candidate and its `value` (-inf from lane n on). `unsure` (a team's lanes agree): not to be
+// had this way (fewer than k finite values, or more candidates than lanes).
 template <int L, int V>
-__device__ __forceinline__ int best_few(const Routing& r, const Team<L>& team, const float (&order)[V],
-                                        float tol, float2* shared, int& n, int& slot, bool& close,
-                                        bool& unsure) {
+__device__ __forceinline__ int few_candidates(const Routing& r, const Team<L>& team,
+                                              const float (&order)[V], float tol, float2* shared,
+                                              float& value, int& n, bool& unsure) {
   int mine = team.rank;
-  float value = order[0];
+  value = order[0];
   n = L;
   if constexpr (V > 1) {
     float sorted[V], top[8];
@@ -404,7 +353,7 @@ __device__ __forceinline__ int best_few(const Routing& r, const Team<L>& team, c
       if (team.rank >= o) upto += before;
     }
     n = team.from(upto, L - 1);
-    if (n > L) {
+    if (n > L || n < r.k) {  // less than k: an infinite bound
       unsure = true;
       return 0;
     }
@@ -421,56 +370,6 @@ __device__ __forceinline__ int best_few(const Routing& r, const Team<L>& team, c
       mine = __float_as_int(got.y);
     }
   }
-  slot = 0;
-  if (tol < 0.f) {
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-      if (V > 1 && j >= n) break;
-      const float other = team.from(value, j);
-      slot += other > value || (other == value && j < team.rank);
-    }
-  } else {
-    bool near = false;
-    const float reach = 2.f * tol + 0x1p-22f * fabsf(value);
-    for (int j = 0; j < n; ++j) {
-      const float other = team.from(value, j);
-      slot += other > value || (other == value && j < team.rank);
-      near |= j != team.rank && !(fabsf(other - value) > reach);
-    }
-    close = __any_sync(team.mask, near && slot < r.k);
-  }
-  if (V == 1) unsure = __any_sync(team.mask, slot < r.k && value == -INFINITY);
-  return mine;
-}
-
-// The k best of the open groups by their values in double: lane j < k returns its expert.
-template <int L, int V>
-__device__ __forceinline__ int best_in_double(const Routing& r, const Team<L>& team,
-                                              const Groups<L, V>& groups, unsigned stay,
-                                              const double (&order)[V]) {
-  unsigned long long key[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    key[v] = team.rank * V + v < r.E && groups.stays(stay, v) ? ordered(order[v]) : 0ull;
-  int mine = 0;
-  for (int j = 0; j < r.k; ++j) {
-    unsigned long long top = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) top = key[v] > top ? key[v] : top;
-    const unsigned long long m = team.max(top);
-    const int src = __ffs(__ballot_sync(team.mask, top == m)) - 1;
-    int at = 0;
-#pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-      if (key[v] == m) at = v;
-    if ((int)(threadIdx.x & 31) == src) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (v == at) key[v] = 0;
-    }
-    at = __shfl_sync(team.mask, at, src);
-    if (j == team.rank) mine = (src - team.base) * V + at;
-  }
   return mine;
 }
 
@@ -484,106 +383,160 @@ __device__ __forceinline__ double sum_in_double(const Team<L>& team, const float
   return team.sum(total);
 }
 
-// All values of a token in double: s + bias, and with no bias the logits where a group is
-// judged by one expert.
+// Slot `slot` < k of each lane (expert `mine`, logit `ls`; the slots' lanes are below `reduce`, a
+// power of two) to the outputs: weights in double, one lane per slot, rounded once. s: the
+// lane's sigmoid.
 template <typename T, int L, int V>
-__device__ __forceinline__ void values_in_double(const Routing& r, const Team<L>& team, const T* row,
-                                                 const float* bias, double (&value)[V]) {
-  float l[V];
-  load_logits<T, V>(row, team.rank, r.E, false, l);
-  float mx = -INFINITY;
+__device__ __forceinline__ void write_slots(const Routing& r, const Team<L>& team, const T* row,
+                                            int64_t t, int mine, float ls, double s, int slot,
+                                            int reduce, int vec, int32_t* idx_out, float* w_out) {
+  const bool chosen = slot < r.k;
+  if (!chosen) {
+    ls = -INFINITY;
+    s = 0.0;
+  }
+  if (!r.sigmoid) {
+    s = 0.0;
+    if (r.renorm) {  // the sum over all experts cancels
+      float most = ls;
+      for (int o = reduce >> 1; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(team.mask, most, o));
+      if (ls > -INFINITY) s = exp((double)ls - (double)most);
+    } else {
+      float l[V], mx = -INFINITY;
+      load_logits<T, V>(row, team.rank, r.E, vec, l);
 #pragma unroll
-  for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
-  mx = team.max(mx);
-  const double total = r.sigmoid ? 1.0 : sum_in_double(team, l, mx);
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = team.rank * V + v;
-    value[v] = 0.0;
-    if (l[v] > -INFINITY)
-      value[v] = r.sigmoid ? 1.0 / (1.0 + exp(-(double)l[v])) : exp((double)l[v] - (double)mx) / total;
-    if (bias) {
-      value[v] += e < r.E ? (double)__ldg(bias + e) : 0.0;
-      if (!(value[v] == value[v])) value[v] = -INFINITY;
-    } else if (r.group_top == 1) {
-      value[v] = l[v];
+      for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
+      mx = team.max(mx);
+      const double total = sum_in_double(team, l, mx);
+      if (ls > -INFINITY) s = exp((double)ls - (double)mx) / total;
     }
   }
+  if (r.renorm) {
+    double all = s;
+    for (int o = reduce >> 1; o > 0; o >>= 1) all += __shfl_xor_sync(team.mask, all, o);
+    s = all > 0.0 ? s / all : 0.0;
+  }
+  if (chosen) {
+    idx_out[t * r.k + slot] = mine;
+    w_out[t * r.k + slot] = (float)(s * (double)r.scale);
+  }
 }
 
-// The groups that stay, decided in double; and the whole choice: the expert of lane `rank` < k.
-// Apart from the kernel, whose registers they would crowd.
-template <typename T, int L, int V>
-__device__ __noinline__ unsigned groups_in_double(const Routing r, const T* row, const float* bias,
-                                                  double* shared) {
-  const Team<L> team;
-  const Groups<L, V> groups(r, team);
-  double value[V];
-  values_in_double<T, L, V>(r, team, row, bias, value);
-  bool close = false;
-  return open_groups<false>(r, team, groups, value, 0.0, shared, close);
-}
-template <typename T, int L, int V>
-__device__ __noinline__ int choose_in_double(const Routing r, const T* row, const float* bias,
-                                             unsigned stay) {
-  const Team<L> team;
-  const Groups<L, V> groups(r, team);
-  double value[V];
-  if (bias) {
-    values_in_double<T, L, V>(r, team, row, bias, value);
-  } else {
-    float l[V];
-    load_logits<T, V>(row, team.rank, r.E, false, l);
-#pragma unroll
-    for (int v = 0; v < V; ++v) value[v] = l[v];
-  }
-  return best_in_double(r, team, groups, stay, value);
+__device__ __forceinline__ double sigmoid_in_double(float l) {
+  return l > -INFINITY ? 1.0 / (1.0 + exp(-(double)l)) : 0.0;
 }
 
-// The place of the lane's candidate among n, one to a lane, by their s + bias in double.
-template <typename T, int L, int V>
-__device__ __noinline__ int reorder_in_double(const Routing r, const T* row, const float* bias, int mine,
-                                              int n) {
-  const Team<L> team;
-  double total = 1.0;
-  float mx = 0.f;
-  if (!r.sigmoid) {
-    float l[V];
-    load_logits<T, V>(row, team.rank, r.E, false, l);
-    mx = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
-    mx = team.max(mx);
-    total = sum_in_double(team, l, mx);
+// A token with every comparison in double, by a whole warp. Few tokens come here, but the
+// kernel ends with the last of them, and what they wait for is this code itself, which is in
+// no cache: so it is short, loops over shared memory (E doubles) and is not unrolled.
+template <typename T, int V>
+__device__ __noinline__ void route_in_double(const Routing r, const T* row, const float* bias, int64_t t,
+                                             double* shared, int32_t* idx_out, float* w_out) {
+  const Team<32> team;
+  const auto at_expert = [](int e) { return e + (e >> 5); };
+  const int gs = r.E / r.groups;
+  float mx = -INFINITY;
+  for (int e = team.rank; e < r.E; e += 32) mx = fmaxf(mx, clean(logit_at(row + e)));
+  mx = team.max(mx);
+  double total = 0.0;
+  __syncwarp();
+#pragma unroll 1
+  for (int e = team.rank; e < r.E; e += 32) {
+    const float l = clean(logit_at(row + e));
+    const double x = l > -INFINITY ? exp(r.sigmoid ? -(double)l : (double)l - (double)mx) : 0.0;
+    shared[at_expert(e)] = x;
+    total += x;
   }
-  const bool in = team.rank < n;
-  double c = -INFINITY;
-  if (in) {
-    const float l = clean(logit_at(row + mine)), b = bias[mine];
-    c = 0.0;
-    if (l > -INFINITY) c = r.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)mx) / total;
-    c += (double)b;
-    if (!(c == c)) c = -INFINITY;
+  total = team.sum(total);
+#pragma unroll 1
+  for (int e = team.rank; e < r.E; e += 32) {
+    const float l = clean(logit_at(row + e));
+    double c = 0.0;
+    if (l > -INFINITY)
+      c = r.sigmoid ? 1.0 / (1.0 + shared[at_expert(e)]) : shared[at_expert(e)] / total;
+    if (bias) c += (double)__ldg(bias + e);
+    if (!bias && r.group_top == 1) c = l;
+    shared[at_expert(e)] = c == c ? c : -INFINITY;
   }
-  int above = 0;
-  for (int j = 0; j < n; ++j) {
-    const double other = team.from(c, j);
-    const int e = team.from(mine, j);
-    above += other > c || (other == c && e < mine);
+  __syncwarp();
+  unsigned stay = 0xffffffffu;
+  if (r.groups > 1) {  // lane g has group g's value: the largest left, group_top times
+    double value = -INFINITY;
+    if (team.rank < r.groups) {
+      value = 0.0;
+      unsigned taken[16] = {};
+#pragma unroll 1
+      for (int m = 0; m < r.group_top; ++m) {
+        double best = -INFINITY;
+        int at = -1;
+#pragma unroll 1
+        for (int i = 0; i < gs; ++i) {
+          const double c = shared[at_expert(team.rank * gs + i)];
+          if (!(taken[i >> 5] >> (i & 31) & 1u) && (at < 0 || c > best)) {
+            best = c;
+            at = i;
+          }
+        }
+        value += best;
+        taken[at >> 5] |= 1u << (at & 31);
+      }
+    }
+    int above = 0;
+#pragma unroll 1
+    for (int j = 0; j < r.groups; ++j) {
+      const double other = team.from(value, j);
+      above += other > value || (other == value && j < team.rank);
+    }
+    stay = __ballot_sync(team.mask, above < r.topk_groups);
   }
-  return in ? above : L;
+  __syncwarp();
+  // with no bias the logits order the experts; a closed or taken one is a NaN
+#pragma unroll 1
+  for (int e = team.rank; e < r.E; e += 32) {
+    if (!bias) shared[at_expert(e)] = clean(logit_at(row + e));
+    if (r.groups > 1 && !(stay >> (e / gs) & 1u)) shared[at_expert(e)] = __longlong_as_double(-1ll);
+  }
+  int mine = 0;
+#pragma unroll 1
+  for (int j = 0; j < r.k; ++j) {
+    double best = 0.0;
+    int at = 0x7fffffff;
+#pragma unroll 1
+    for (int e = team.rank; e < r.E; e += 32) {
+      const double c = shared[at_expert(e)];
+      if (c == c && (at == 0x7fffffff || c > best)) {
+        best = c;
+        at = e;
+      }
+    }
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) {
+      const double b2 = __shfl_xor_sync(team.mask, best, o);
+      const int a2 = __shfl_xor_sync(team.mask, at, o);
+      if (a2 != 0x7fffffff && (at == 0x7fffffff || b2 > best || (b2 == best && a2 < at))) {
+        best = b2;
+        at = a2;
+      }
+    }
+    if (at % 32 == team.rank) shared[at_expert(at)] = __longlong_as_double(-1ll);
+    if (j == team.rank) mine = at;
+  }
+  const float ls = team.rank < r.k ? clean(logit_at(row + mine)) : -INFINITY;
+  write_slots<T, 32, V>(r, team, row, t, mine, ls, sigmoid_in_double(ls), team.rank, 32, 0, idx_out, w_out);
+  __syncwarp();
 }
 
 // Routing, one team of L lanes per token. The logits alone decide where nothing else is
 // asked for (both scores rise with the logit, so fp32 is exact); else the values s + bias
-// and the groups' sums are formed in fp32 with the approximate exponential and reciprocal, and what
-// lies within its error bounds of a decision is decided in double: the order of the
-// candidates from their own values (one a lane), the groups, long rows of ties and rows
-// with fewer than k finite values from all values. Bounds, with u = 2^-24: the exponential is
-// off by 4 u and by 1.5 u |x| for its argument, the reciprocal by 2 u; s (1 - s) is at most
-// 1/4 and |x| s (1 - s) at most 0.23, so a sigmoid is off by less than 5 u (6 u are allowed); |x| e^x
-// is at most 0.37 below 0, so a softmax is off by less than 32 u of the largest probability (its
-// sum of up to 512 terms is a tree of 20 levels); the sum with the bias by u of its value.
+// and the groups' sums are formed in fp32 with the approximate exponential and reciprocal: they
+// give the groups and the candidates, which under sigmoid scores are then ordered by their own
+// s + bias in double. A token with another decision within its error bounds is put aside and
+// routed in double after up to 32 others of the team (a few in ten thousand). Bounds, with
+// u = 2^-24: the exponential is off by 4 u and by 1.5 u |x| for its argument, the reciprocal by
+// 2 u; s (1 - s) is at most 1/4 and |x| s (1 - s) at most 0.23, so a sigmoid is off by less than 5 u
+// (6 u are allowed); |x| e^x is at most 0.37 below 0, so a softmax is off by less than 32 u of the
+// largest probability (its sum of up to 512 terms is a tree of 20 levels); the sum with the bias
+// by u of its value.
 //
 // Bound by instructions, not bytes: a team is as narrow as 16 values per lane allow, so that
 // a warp's instruction serves up to four tokens.
@@ -609,18 +562,11 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
     }
     __syncthreads();
   }
-  for (int64_t t0 = (int64_t)blockIdx.x * kPer; t0 < r.T; t0 += (int64_t)gridDim.x * kPer) {
-    const int64_t t = t0 + threadIdx.x / L;
-    if (t >= r.T) continue;  // a token's lanes leave together
-    const T* row = logits + t * r.stride;
+  // true where the token is done
+  const auto route = [&](const T* row, int64_t t) {
     float l[V], c[V];
     load_logits<T, V>(row, team.rank, r.E, vec, l);
-    float mx = -INFINITY, tol = 0.f;
-    if (!r.sigmoid && (scores || !r.renorm)) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
-      mx = team.max(mx);
-    }
+    float tol = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) c[v] = l[v];
     if (scores) {
@@ -629,7 +575,10 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
         for (int v = 0; v < V; ++v) c[v] = fast_rcp(1.f + fast_exp2(-kLog2e * l[v]));
         tol = 0x1.8p-22f;
       } else {
-        float sum = 0.f;
+        float mx = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) mx = fmaxf(mx, l[v]);
+        mx = team.max(mx);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           c[v] = l[v] > -INFINITY ? fast_exp2(kLog2e * (l[v] - mx)) : 0.f;
@@ -648,12 +597,9 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
     }
     unsigned stay = 0xffffffffu;
     if (r.groups > 1) {
-      bool near = r.group_top > 2;
-      if (!near) {
-        stay = open_groups<true>(r, team, groups, c, tol, reinterpret_cast<float*>(shared), near);
-        near = scores && near;
-      }
-      if (near) stay = groups_in_double<T, L, V>(r, row, bias, shared);
+      bool near = false;
+      stay = open_groups(r, team, groups, c, tol, reinterpret_cast<float*>(shared), near);
+      if (scores && near) return false;
     }
     if (bias) {
 #pragma unroll
@@ -670,43 +616,74 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
       }
     }
     int mine, n = 0, slot = team.rank;
-    bool near = false, unsure = false;
+    bool unsure = false;
     if constexpr (FEW) {
-      mine = best_few(r, team, l, bias ? tol : -1.f, reinterpret_cast<float2*>(shared), n, slot, near, unsure);
+      float value;
+      mine = few_candidates(r, team, l, bias ? tol : -1.f, reinterpret_cast<float2*>(shared), value, n, unsure);
+      if (unsure) return false;
+      if (!bias || !r.sigmoid) {  // by value: exact, or with no two of the chosen too close
+        const float reach = bias ? 2.f * tol + 0x1p-22f * fabsf(value) : -1.f;
+        bool near = false;
+        slot = 0;
+        for (int j = 0; j < n; ++j) {
+          const float other = team.from(value, j);
+          slot += other > value || (other == value && j < team.rank);
+          near |= j != team.rank && !(fabsf(other - value) > reach);
+        }
+        unsure = __any_sync(team.mask, slot < r.k && (value == -INFINITY || (bias && near)));
+      } else if (V == 1) {  // all experts are candidates
+        const int finite = __popc(__ballot_sync(team.mask, value > -INFINITY));
+        unsure = finite < r.k;
+      }
     } else {
+      bool near = false;
       mine = best_experts(r, team, l, bias ? tol : -1.f, reinterpret_cast<float*>(shared), n, near);
-      unsure = n == 0;
+      unsure = n == 0 || (near && !r.sigmoid);
     }
-    if (unsure) {
-      mine = choose_in_double<T, L, V>(r, row, bias, stay);
-      slot = team.rank;
-    } else if (near) {
-      slot = reorder_in_double<T, L, V>(r, row, bias, mine, n);
+    if (unsure) return false;
+    // the chosen are among the first n lanes
+    const bool real = team.rank < n && mine < r.E;
+    const float ls = real ? clean(logit_at(row + mine)) : -INFINITY;
+    const double sg = r.sigmoid ? sigmoid_in_double(ls) : 0.0;
+    if (bias && r.sigmoid) {  // the candidates' own values, which the weights need anyhow
+      const bool open = real && (V > 1 || !FEW || l[0] > -INFINITY);
+      const double c = open ? sg + (double)s_bias[mine] : -INFINITY;
+      slot = 0;
+      for (int j = 0; j < n; ++j) {
+        const double other = team.from(c, j);
+        const int e = team.from(mine, j);
+        slot += other > c || (other == c && e < mine);
+      }
+      if (!real) slot = r.k;
     }
-    // weights: one lane per slot, in double, rounded once
-    const bool chosen = slot < r.k;
-    const float ls = chosen ? clean(logit_at(row + mine)) : -INFINITY;
-    const int reduce = n > pairs ? L : pairs;  // the chosen are among the first lanes
-    double s = 0.0;
-    if (r.sigmoid) {
-      if (ls > -INFINITY) s = 1.0 / (1.0 + exp(-(double)ls));
-    } else if (r.renorm) {  // the sum over all experts cancels
-      float most = ls;
-      for (int o = reduce >> 1; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(team.mask, most, o));
-      if (ls > -INFINITY) s = exp((double)ls - (double)most);
+    write_slots<T, L, V>(r, team, row, t, mine, ls, sg, slot, n > pairs ? L : pairs, vec, idx_out, w_out);
+    return true;
+  };
+  const int64_t stride = (int64_t)gridDim.x * kPer;
+  constexpr int kTeams = 32 / L;
+  // of the warp's first team; its lanes stay together for the tokens put aside
+  for (int64_t t0 = (int64_t)blockIdx.x * kPer + threadIdx.x / 32 * kTeams; t0 < r.T; t0 += 32 * stride) {
+    unsigned aside = 0;
+    if (r.group_top > 2) {
+      aside = 0xffffffffu;
     } else {
-      load_logits<T, V>(row, team.rank, r.E, vec, l);
-      const double total = sum_in_double(team, l, mx);
-      if (ls > -INFINITY) s = exp((double)ls - (double)mx) / total;
+      for (int i = 0; i < 32; ++i) {
+        const int64_t t = t0 + team.base / L + i * stride;
+        if (t >= r.T) break;  // a token's lanes leave together
+        if (!route(logits + t * r.stride, t)) aside |= 1u << i;
+      }
     }
-    if (r.renorm) {
-      double all = s;
-      for (int o = reduce >> 1; o > 0; o >>= 1) all += __shfl_xor_sync(team.mask, all, o);
-      s = all > 0.0 ? s / all : 0.0;
-    }
-    if (chosen) {
-      idx_out[t * r.k + slot] = mine;
-      w_out[t * r.k + slot] = (float)(s * (double)r.scale);
+    __syncwarp();
+    if (__ballot_sync(0xffffffffu, aside != 0) == 0) continue;
+#pragma unroll
+    for (int q = 0; q < kTeams; ++q) {
+      unsigned left = __shfl_sync(0xffffffffu, aside, q * L);
+      for (; left; left &= left - 1) {
+        const int64_t t = t0 + q + (__ffs(left) - 1) * stride;
+        if (t < r.T)
+          route_in_double<T, (L * V + 31) / 32>(r, logits + t * r.stride, bias, t, s_value[threadIdx.x / 32 * kTeams],
+                                                idx_out, w_out);
+      }
     }
   }
 }

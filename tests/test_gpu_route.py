@@ -127,10 +127,19 @@ def test_route_near_ties_are_decided_exactly(e, k, groups, top, m, scoring):
 def test_route_huge_biases():
     l = _logits(64, 64, 3, "normal")
     g = torch.Generator().manual_seed(8)
-    for size in (1e3, 1e30, 3e38):
-        bias = torch.randint(-1, 2, (64,), generator=g).float() * size
+    for size in (1e3, 1e30, 3e38, float("inf")):
+        sign = torch.randint(-1, 2, (64,), generator=g).float()
+        bias = torch.where(sign == 0, 0.0, sign * size)
         _check_route(l, M.Routing(5, "sigmoid", 8, 3, 2), bias)
         _check_route(l, M.Routing(5, "softmax"), bias)
+
+
+def test_route_zero_bias_and_bf16_ties():
+    """A bias of zeros (before its first update) over bf16 logits: exact ties in most rows."""
+    for t in (300, 5000):
+        l = _logits(t, 64, t, "normal", torch.bfloat16)
+        for r in (M.Routing(8, "sigmoid"), M.Routing(6, "softmax"), M.Routing(8, "sigmoid", 8, 4, 2)):
+            _check_route(l, r, torch.zeros(64))
 
 
 def test_route_matches_the_layers_router():
