@@ -190,13 +190,20 @@ struct Groups {
   }
 };
 
+__device__ __forceinline__ double sigmoid_in_double(float l) {
+  return l > -INFINITY ? 1.0 / (1.0 + exp(-(double)l)) : 0.0;
+}
+
 // The groups that stay, as a ballot (bit base + g * lanes for group g). A value may be off by
 // tol + 2 u |value|; `close` is set where the last group that stays and the first that goes
 // are not further apart than that allows. A group's one or two best: its lanes take their own
-// values, or every lanes-th from shared memory, and merge their pairs.
-template <int L, int V>
+// values, or every lanes-th from shared memory, and merge their pairs. Close groups of
+// sigmoid scores are judged again by the values in double of those experts that can be
+// among their best.
+template <typename T, int L, int V>
 __device__ __forceinline__ unsigned open_groups(const Routing& r, const Team<L>& team,
-                                                const Groups<L, V>& groups, const float (&value)[V],
+                                                const Groups<L, V>& groups, const T* row,
+                                                const float* bias, const float (&value)[V],
                                                 float tol, float* shared, bool& close) {
   const int lanes = groups.lanes, g = team.rank / lanes;
   const auto at_expert = [](int e) { return e + (e >> 5); };  // groups of 32 on distinct banks
@@ -235,8 +242,44 @@ __device__ __forceinline__ unsigned open_groups(const Routing& r, const Team<L>&
   // what a group's value may be off by: its terms' bounds and their sum's rounding
   const float off = real ? 2 * tol + 0x1p-22f * (fabsf(m1) + (r.group_top == 2 ? fabsf(m2) : 0.f)) : 0.f;
   const float least = -team.max(real && in ? -mine : -INFINITY), most = team.max(real && !in ? mine : -INFINITY);
-  close = r.topk_groups < r.groups && !(least - most > 2 * team.max(off));
-  return __ballot_sync(team.mask, in);
+  const float reach = 2 * team.max(off);
+  close = r.topk_groups < r.groups && !(least - most > reach);
+  if (!close || !r.sigmoid) return __ballot_sync(team.mask, in);
+  close = false;
+  if (own) {
+    __syncwarp(team.mask);
+#pragma unroll
+    for (int v = 0; v < V; ++v) shared[at_expert(team.rank * V + v)] = value[v];
+    __syncwarp(team.mask);
+  }
+  double d1 = -INFINITY, d2 = -INFINITY;
+  const float least_of_two = reach < INFINITY ? (r.group_top == 2 ? m2 : m1) - reach : -INFINITY;
+  if (g < r.groups) {
+#pragma unroll 1
+    for (int i = team.rank - g * lanes; i < groups.size; i += lanes) {
+      const int e = g * groups.size + i;
+      if (!(shared[at_expert(e)] >= least_of_two)) continue;
+      double c = sigmoid_in_double(clean(logit_at(row + e)));
+      if (bias) c += (double)__ldg(bias + e);
+      if (!(c == c)) c = -INFINITY;
+      d2 = fmax(d2, fmin(c, d1));
+      d1 = fmax(d1, c);
+    }
+  }
+#pragma unroll 1
+  for (int o = lanes >> 1; o > 0; o >>= 1) {
+    const double o1 = __shfl_xor_sync(team.mask, d1, o), o2 = __shfl_xor_sync(team.mask, d2, o);
+    d2 = fmax(fmax(d2, o2), fmin(d1, o1));
+    d1 = fmax(d1, o1);
+  }
+  const double exact = r.group_top == 2 ? d1 + d2 : d1;
+  above = 0;
+#pragma unroll 1
+  for (int j = 0; j < r.groups; ++j) {
+    const double other = team.from(exact, j * lanes);
+    above += other > exact || (other == exact && j < g);
+  }
+  return __ballot_sync(team.mask, above < r.topk_groups);
 }
 
 // The best experts in order, one to a lane; order[v] compares them, -inf is none. Returns
@@ -422,10 +465,6 @@ __device__ __forceinline__ void write_slots(const Routing& r, const Team<L>& tea
   }
 }
 
-__device__ __forceinline__ double sigmoid_in_double(float l) {
-  return l > -INFINITY ? 1.0 / (1.0 + exp(-(double)l)) : 0.0;
-}
-
 // A token with every comparison in double, by a whole warp. Few tokens come here, but the
 // kernel ends with the last of them, and what they wait for is this code itself, which is in
 // no cache: so it is short, loops over shared memory (E doubles) and is not unrolled.
@@ -598,7 +637,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
     unsigned stay = 0xffffffffu;
     if (r.groups > 1) {
       bool near = false;
-      stay = open_groups(r, team, groups, c, tol, reinterpret_cast<float*>(shared), near);
+      stay = open_groups(r, team, groups, row, bias, c, tol, reinterpret_cast<float*>(shared), near);
       if (scores && near) return false;
     }
     if (bias) {

@@ -134,6 +134,18 @@ def test_route_huge_biases():
         _check_route(l, M.Routing(5, "softmax"), bias)
 
 
+def test_route_a_single_infinite_bias():
+    for t in (50, 5000):
+        l = _logits(t, 64, 4, "normal")
+        for at in (3, 60):
+            bias = 0.05 * torch.randn(64, generator=torch.Generator().manual_seed(at))
+            bias[at] = float("inf")
+            for scoring in ("sigmoid", "softmax"):
+                for top in (1, 2):
+                    idx, _ = _check_route(l, M.Routing(4, scoring, 8, 1, top), bias)
+                    assert (idx[:, 0] == at).all()
+
+
 def test_route_zero_bias_and_bf16_ties():
     """A bias of zeros (before its first update) over bf16 logits: exact ties in most rows."""
     for t in (300, 5000):
