@@ -216,11 +216,13 @@ constexpr int kTileRows = 64;
 constexpr int kChunkK = 64;    // features per stage of the shrink
 constexpr int kStages = 4;     // of the shrink
 constexpr int kChunkN = 64;    // columns per step of the expand
-constexpr int kAhead = 2;      // steps of the expand in flight
+// Steps of the expand in flight beside the one at work: as two blocks an SM have room for.
+__host__ __device__ constexpr int steps_ahead(int out_bytes) { return out_bytes == 4 ? 2 : 3; }
 constexpr int kMaxSlices = 8;  // of the features
 
 // In the workspace: the tiles {adapter or -1, first sorted row, rows, 0}, their count, the
-// sorted row numbers, and t = scale x a^T of each tile in bf16 parts [tile][part][64][RP].
+// sorted row numbers, and t = scale x a^T in bf16 parts [part][R + 64][RP], rows as sorted (a
+// tile's copy of 64 rows runs into the next tile's and, for the last, past R).
 struct Plan {
   int4* tiles;
   int32_t* count;
@@ -457,10 +459,11 @@ __global__ void __launch_bounds__(128) k_shrink_tiles(const Lora l, const Plan p
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n) v[n] *= scale;
-    uint16_t* t = p.t + (int64_t)tile * parts * kTileRows * RP + i * 4;
-    for (int part = 0; part < parts; ++part) {
+    if (i / (RP / 4) >= tl.z) continue;
+    uint16_t* t = p.t + (int64_t)tl.y * RP + i * 4;
+    for (int part = 0; part < parts; ++part, t += (l.R + kTileRows) * RP) {
       const uint2 both = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
-      *reinterpret_cast<uint2*>(t + part * kTileRows * RP) = both;
+      *reinterpret_cast<uint2*>(t) = both;
       v[0] -= lo(both.x);
       v[1] -= hi(both.x);
       v[2] -= lo(both.y);
@@ -500,7 +503,7 @@ struct Vec<__nv_bfloat16> {
 // out = base + t b^T. The tiles' steps of 64 columns, in a row, are cut evenly among as many
 // blocks as run at once; a block takes its steps tile by tile. 8 warps as 4 (16 rows) x 2 (32
 // columns). t's parts times b are exact in fp32; t's fragments stay in registers up to rank 64.
-// base and b come by 16-byte asynchronous copies two steps ahead: what has to be in flight
+// base and b come by 16-byte asynchronous copies two or three steps ahead: what has to be in flight
 // to keep HBM busy (some 50 KB an SM) would not fit the registers beside the sums. b's rows
 // go to shared memory in the order in which a thread's columns of neighbouring 8-wide
 // products are neighbours in out, so that out is written 16 bytes at a time.
@@ -516,7 +519,7 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
   constexpr int kRowBytes = kChunkN * (int)sizeof(T);
   constexpr int kBaseBytes = kTileRows * kRowBytes;
   constexpr int kStepBytes = kBaseBytes + kChunkN * kPitch;
-  constexpr int kPieces = RP / 8;
+  constexpr int kPieces = RP / 8, kAhead = steps_ahead(sizeof(T));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const T* base = static_cast<const T*>(l.base);
   T* out = static_cast<T*>(l.out);
@@ -603,11 +606,13 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
       copies_end();
     };
     __syncthreads();  // the tile before is done with the shared memory
-    const uint16_t* t = p.t + (int64_t)tile * kParts * kTileRows * RP;
+    const uint16_t* t = p.t + (int64_t)tl.y * RP;
 #pragma unroll
     for (int i = 0; i < (kParts * kTileRows * kPieces + 255) / 256; ++i) {
       const int q = tid + 256 * i, row = q / kPieces;  // rows of all parts, one after another
-      if (q < kParts * kTileRows * kPieces) copy16(t_at + row * kPitch + q % kPieces * 16, t + q * 8, true);
+      if (q < kParts * kTileRows * kPieces)
+        copy16(t_at + row * kPitch + q % kPieces * 16,
+               t + ((int64_t)(row / kTileRows) * (l.R + kTileRows) + row % kTileRows) * RP + q % kPieces * 8, true);
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load(first + i, i);
@@ -721,7 +726,7 @@ Plan plan_at(const Lora& l, void* ws, size_t* end) {
   p.order = reinterpret_cast<int32_t*>(at);
   at += up256((size_t)l.R * 4);
   p.t = reinterpret_cast<uint16_t*>(at);
-  at += up256((size_t)max_tiles(l.R, l.G) * (l.fp32 ? 3 : 2) * kTileRows * rank_pad(l.rank) * 2);
+  at += up256((size_t)(l.fp32 ? 3 : 2) * (l.R + kTileRows) * rank_pad(l.rank) * 2);
   *end = (size_t)(at - static_cast<char*>(ws));
   return p;
 }
@@ -745,7 +750,7 @@ cudaError_t run_tiles(const Lora& l, const Plan& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int parts = l.fp32 ? 3 : 2, size = l.fp32 ? 4 : 2;
   const size_t smem = (size_t)parts * kTileRows * (RP * 2 + 16) +
-                      (size_t)(kAhead + 1) * kChunkN * (kTileRows * size + RP * 2 + 16);
+                      (size_t)(steps_ahead(size) + 1) * kChunkN * (kTileRows * size + RP * 2 + 16);
   const dim3 grid((unsigned)(num_sms() * (RP <= 64 ? 2 : 1))), block(256);
   if (l.fp32) {
     e = allow_smem(k_expand_tiles<float, RP>, smem);

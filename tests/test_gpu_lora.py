@@ -115,7 +115,7 @@ def test_ids_outside_the_adapters_are_none(r):
 @pytest.mark.parametrize("r", [4, 500])
 def test_infinities_stay_in_their_rows(r):
     base, x, a, b, ids, scale = _case(r, 128, 72, 16, 4, torch.float32, "mixed", 3)
-    ids[:] = 1
+    ids[:] = (torch.arange(r) % 3).int()
     ids[1] = -1
     x[1] = float("nan")                               # a row without an adapter: never multiplied
     x[2, 5] = float("inf")
@@ -132,6 +132,31 @@ def test_no_rows():
     out = M.lora_add(e(0, 64), e(0, 128, dtype=torch.bfloat16), e(2, 8, 128, dtype=torch.bfloat16).zero_(),
                      e(2, 64, 8, dtype=torch.bfloat16).zero_(), e(0, dtype=torch.int32))
     assert out.shape == (0, 64)
+
+
+def test_many_adapters_few_of_them_used():
+    """Thousands of adapters loaded, rows of three of them and of none; sizes past 32 bits in a."""
+    r, h, n, rank, ad = 300, 8192, 136, 16, 17000 // 2
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a = torch.randn(ad * 2, rank, h, device="cuda", generator=g, dtype=torch.bfloat16)[:16384].contiguous()
+    assert a.numel() > 2 ** 31 - 1
+    b = torch.randn(16384, n, rank, device="cuda", generator=g, dtype=torch.bfloat16) / 4
+    ids = torch.tensor([16383, 5, -1, 16382], dtype=torch.int32, device="cuda").repeat_interleave(75)
+    x = torch.randn(r, h, device="cuda", generator=g, dtype=torch.bfloat16) / 64
+    base = torch.randn(r, n, device="cuda", generator=g)
+    for k in (r, 9):                                 # as tiles, and a row at a time
+        rows = torch.linspace(0, r - 1, k).long().cuda()
+        got = M.lora_add(base[rows], x[rows], a, b, ids[rows])
+        for i in (0, k // 3, k // 2, k - 1):
+            j = int(ids[rows][i])
+            want = base[rows][i].double()
+            if j >= 0:
+                t = a[j].double() @ x[rows][i].double()
+                want = want + b[j].double() @ t
+                mag = b[j].double().abs() @ (a[j].double().abs() @ x[rows][i].double().abs())
+                assert ((got[i].double() - want).abs() <= (h / 32 + 200) * U * (mag + want.abs())).all()
+            else:
+                assert torch.equal(got[i], base[rows][i])
 
 
 @pytest.mark.parametrize("r", [16, 600])
