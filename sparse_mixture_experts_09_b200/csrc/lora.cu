@@ -692,11 +692,14 @@ int rank_pad(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ?
 // tile costs as much for one row as for 64, and the sorting and two more launches some 8 us.
 // Device times, rows / tiles: 64 rows of 4 adapters, rank 64, 4096 -> 14336 features 27 / 20 us,
 // of 64 adapters 36 / 67; 128 rows of 8 adapters, rank 16, 4096 -> 4096 11 / 14 us; 256 rows of 8
-// adapters 20 / 15, of 256 adapters 23 / 41. How many adapters a batch uses is not known here:
-// from 128 rows on the tiles lose less in their worst case than they gain in their best.
+// adapters 20 / 15, of 256 adapters 23 / 41; 192 rows of 192 adapters 17 / 35. How many adapters a
+// batch uses is not known here, only how many there are: from 256 rows on, and for heavy
+// adapters from 128, the tiles lose less in their worst case than they gain in their best.
 bool use_tiles(const Lora& l) {
-  const int64_t adapter_bytes = (int64_t)l.rank * (l.H + l.N) * 2;
-  return l.R >= 128 || (l.R >= 12 * (int64_t)l.G && l.R * adapter_bytes >= (int64_t)64 << 20);
+  const bool light = l.R * (int64_t)l.rank * (l.H + l.N) * 2 < (int64_t)64 << 20;
+  if (l.R < 128) return !light && l.R >= 12 * (int64_t)l.G;
+  if (l.R < 256) return !light || l.R >= 8 * (int64_t)l.G;
+  return true;
 }
 
 // Slices of the features: as many blocks as the SMs hold at once (three each; a second
