@@ -61,6 +61,9 @@ __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __fl
 // Columns: P lanes share one (P the power of two from rank / 8 up), each 8 ranks of it in one
 // 16-byte load; a warp takes 32 columns at a time, P of them per lane group, and adds with a
 // butterfly that leaves one column in every lane.
+//
+// Bound by latency, then by the adapters' bytes: 2 rows, rank 16, 14336 -> 4096 features 6.1 us;
+// 61 rows of 128 adapters, 4096 -> 14336 11.8 us, 32.7 MB, 2.8 TB/s.
 template <typename T, int P>
 __global__ void __launch_bounds__(kThreads) k_lora_rows(const Lora l) {
   pdl_trigger();
@@ -209,8 +212,10 @@ cudaError_t few_rows(const Lora& l, cudaStream_t st) {
 //
 // The work is bound by HBM: out and base at 2 or 4 bytes an element against 2 * rank
 // operations (times the parts of t, below), so mma.sync, whose fragments feed straight
-// from shared memory and whose sums lie in the registers that hold base, is fast enough
-// and a tensor-memory pipeline would have nothing to hide.
+// from shared memory and whose sums lie in registers beside base, is fast enough:
+// with two thirds of the products left out the expand takes the same time.
+// 4096 rows of 16 adapters, rank 64, 4096 -> 14336 features, fp32: 125 us (plan 6, shrink 18,
+// expand 100, which moves 470 MB at 4.7 TB/s; the floor of all is 82 us).
 
 constexpr int kTileRows = 64;
 constexpr int kChunkK = 64;    // features per stage of the shrink
