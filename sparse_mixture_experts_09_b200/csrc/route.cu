@@ -34,9 +34,11 @@ __device__ __forceinline__ float fast_rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// sigmoid(l) and 1 - sigmoid(l), each to within a few units of its own last place.
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sigmoid(l) and 1 - sigmoid(l), each to within (8 + 1.5 |l|) 2^-24 of itself.
 __device__ __forceinline__ void sigmoid_pair(float l, float& s, float& rest) {
-  const float x = expf(-fabsf(l)), big = fast_rcp(1.f + x), small = x * big;
+  const float x = fast_exp2(-kLog2e * fabsf(l)), big = fast_rcp(1.f + x), small = x * big;
   s = l >= 0.f ? big : small;
   rest = l >= 0.f ? small : big;
 }
@@ -143,7 +145,6 @@ __device__ __forceinline__ void store_row(T* row, int rank, int E, bool vec, con
   }
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Descending, by Batcher's odd-even merge (all indices are known at compile time).
 template <int V>
@@ -782,7 +783,7 @@ __device__ __forceinline__ void block_losses(const Routing& r, const T* __restri
     float x[V], sum = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      x[v] = expf(l[v] - top);
+      x[v] = fast_exp2(kLog2e * (l[v] - top));
       sum += x[v];
     }
     sum = team.sum(sum);
@@ -1035,7 +1036,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
       float sum = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        p[v] = expf(l[v] - top);
+        p[v] = fast_exp2(kLog2e * (l[v] - top));
         sum += p[v];
       }
       sum = team.sum(sum);
@@ -1079,7 +1080,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
         if (my_e >= 0) sigmoid_pair(ls, u, rest);
       } else if (r.renorm) {
         const float top = slots_max(ls);
-        if (ls > -INFINITY) u = expf(ls - top);
+        if (ls > -INFINITY) u = fast_exp2(kLog2e * (ls - top));
       }
       float term = 0.f;  // what slot `rank` adds to its expert
       if (r.renorm) {

@@ -6,10 +6,10 @@ Tolerances, derived:
 - weights: computed in double and rounded once to fp32: 2^-24 of the value (2^-149 below
   the normal range).
 - losses and gradient: fp32 terms. With u = 2^-24 and R the largest |l - max l| that has
-  weight: an exponential is off by 4u (two ulp) + R u (its argument's rounding), a sum over
-  E <= 512 experts by (V + 5) u <= 21 u, so a probability by 2 (4 + R) + 21 + 2 < 32 + 2R u;
-  a gradient term multiplies two such factors and adds k <= 32 products: 128 + 4R u of the
-  magnitudes that are added up. Sums over tokens are double but for at most 64 fp32
+  weight: an exponential is off by 4u (2^-22) + 1.5 R u (its argument's rounding), and weighted by
+  itself by less than 5u, a sum over E <= 512 experts by (V + 5) u <= 21 u, so a probability by
+  4 + 1.5 R + 5 + 21 + 2 <= 32 + 2R u; a gradient term multiplies two such factors and adds k <= 32
+  products: 128 + 4R u of the magnitudes that are added up. Sums over tokens are double but for at most 64 fp32
   additions per lane: 64 u more."""
 import numpy as np
 import pytest
