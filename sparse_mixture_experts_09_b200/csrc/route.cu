@@ -1091,7 +1091,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
         term = u * rest * g;
       } else {
         float gp = 0.f;
-        if (my_e >= 0 && ls > -INFINITY) u = expf(ls - lse);
+        if (my_e >= 0 && ls > -INFINITY) u = fast_exp2(kLog2e * (ls - lse));
         gp = team.sum(g * u);  // every lane needs it
         term = u * g;
 #pragma unroll
