@@ -582,7 +582,7 @@ __device__ __noinline__ void route_in_double(const Routing r, const T* row, cons
 // the issue slots taken): a team is as narrow as 16 values per lane allow, so that a warp's
 // instruction serves up to four tokens. Device times: 16384 tokens, 256 experts, 8 slots, sigmoid
 // scores, bias, 4 of 8 groups 24.6 us (17.8 MB: 2.7 us at HBM's rate), without groups 18.7, by
-// logits alone 19.7; 65536 x 64 24 us; one token 3.4 us.
+// logits alone 19.7; 65536 x 64 24 us; one token 3.3 us.
 template <typename T, int L, int V, bool FEW>
 __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
     k_route(const Routing r, const T* __restrict__ logits, const float* __restrict__ bias, int vec,
@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
 // adds its experts' p over the block's tokens in fp32 (at most a few dozen), the block
 // adds its teams' sums in order in double: E + 1 sums and counts. Bound by latency: few bytes
 // and few steps per token, so the next token's loads go out before this one's sums (65521
-// tokens, 64 experts, 6 slots: 17.9 us with the second pass; 18.4 MB, 2.8 us at HBM's rate).
+// tokens, 64 experts, 6 slots: 17.0 us with the second pass; 18.4 MB, 2.8 us at HBM's rate).
 template <typename T, int L, int V, int WARPS>
 __device__ __forceinline__ void block_losses(const Routing& r, const T* __restrict__ logits,
                                              const int32_t* __restrict__ idx,
@@ -970,8 +970,8 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
 //   balance: softmax p_e (c_e - sum c p); sigmoid s_e (1 - s_e) (c_e - sum c p) / sum s;
 //   z: 2 d1 / N * logsumexp * softmax_e.
 // A slot's term crosses from its lane to its expert's through shared memory. Bound by
-// instructions (690 a token at 256 experts, 64% of the issue slots): 16384 x 256 with sigmoid scores
-// and losses 18.7 us (34.6 MB: 5.3 us at HBM's rate), 4096 x 8 4.5 us.
+// instructions (580 a token at 256 experts, 57% of the issue slots): 16384 x 256 with sigmoid scores
+// and losses 16.9 us (34.6 MB: 5.3 us at HBM's rate), 4096 x 8 4.4 us.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
     k_route_bwd(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
