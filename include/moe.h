@@ -527,7 +527,8 @@ moe_status_t moe_router_losses(const moe_routing_t* routing, const void* logits,
  *   d_topk_w [T, k] fp32, nullable (no weight term);
  *   counts [E + 1] int32 from moe_router_losses and d_losses [2] fp32 (device), both or
  *     neither NULL (no loss terms); token_mask [T] uint8, nullable: the losses' mask;
- *   d_logits [T, E] out, contiguous, of the logits' type: fp32 arithmetic, one rounding. */
+ *   d_logits [T, E] out, contiguous, of the logits' type, no overlap with the inputs: fp32
+ *     arithmetic, one rounding. An expert named more than once gets the sum of its slots. */
 moe_status_t moe_route_backward(const moe_routing_t* routing, const void* logits,
                                 const int32_t* topk_idx, const float* d_topk_w,
                                 const int32_t* counts, const float* d_losses,

@@ -1097,28 +1097,39 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
 #pragma unroll
         for (int v = 0; v < V; ++v) dl[v] -= p[v] * gp;
       }
-      // from the slots' lanes to their experts'
+      // From the slots' lanes to their experts': plain stores, and where a list names an expert
+      // more than once (a slot does not find its own rank again) additions in the slots' order.
+      float* own = slots + team.rank * V;
       __syncwarp(team.mask);
       if constexpr (V % 4 == 0) {
-        float4* own = reinterpret_cast<float4*>(slots + team.rank * V);
 #pragma unroll
-        for (int v = 0; v < V / 4; ++v) own[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-        __syncwarp(team.mask);
-        if (my_e >= 0) atomicAdd(slots + my_e, term);
-        __syncwarp(team.mask);
+        for (int v = 0; v < V; v += 4) *reinterpret_cast<float4*>(own + v) = make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
 #pragma unroll
-        for (int v = 0; v < V / 4; ++v) {
-          const float4 f = own[v];
-          dl[4 * v] += f.x, dl[4 * v + 1] += f.y, dl[4 * v + 2] += f.z, dl[4 * v + 3] += f.w;
+        for (int v = 0; v < V; ++v) own[v] = 0.f;
+      }
+      __syncwarp(team.mask);
+      if (my_e >= 0) slots[my_e] = (float)team.rank;
+      __syncwarp(team.mask);
+      const bool shared = my_e >= 0 && slots[my_e] != (float)team.rank;
+      const bool any = __any_sync(team.mask, shared);  // every lane has read by then
+      if (my_e >= 0) slots[my_e] = any ? 0.f : term;
+      __syncwarp(team.mask);
+      if (any) {
+        for (int s = 0; s < r.k; ++s) {
+          if (my_e >= 0 && team.rank == s) slots[my_e] += term;
+          __syncwarp(team.mask);
+        }
+      }
+      if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(own + v);
+          dl[v] += f.x, dl[v + 1] += f.y, dl[v + 2] += f.z, dl[v + 3] += f.w;
         }
       } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) slots[team.rank * V + v] = 0.f;
-        __syncwarp(team.mask);
-        if (my_e >= 0) atomicAdd(slots + my_e, term);
-        __syncwarp(team.mask);
-#pragma unroll
-        for (int v = 0; v < V; ++v) dl[v] += slots[team.rank * V + v];
+        for (int v = 0; v < V; ++v) dl[v] += own[v];
       }
     }
     store_row<T, V>(d_logits + t * r.E, team.rank, r.E, vec_out, dl);

@@ -256,6 +256,29 @@ def test_backward_ignores_slots_that_name_no_expert():
     assert M.router_losses(l, idx, r).counts[:8].sum().item() == 18
 
 
+@pytest.mark.parametrize("e,k", [(8, 3), (16, 8), (64, 6), (128, 7), (40, 24), (256, 8), (512, 32)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_backward_of_repeated_experts(e, k, scoring, renorm):
+    """An expert named more than once gets the sum of its slots, the same bits each time (up to
+    31 more roundings than distinct slots cost)."""
+    t = 700
+    g = torch.Generator().manual_seed(e * k)
+    l = _logits(t, e, e + k, "normal")
+    idx = torch.randint(0, e, (t, k), generator=g, dtype=torch.int32)
+    idx[::3] = idx[::3, :1]                              # one expert in every slot
+    idx[1::3] %= 3
+    d_w = torch.randn(t, k, generator=g)
+    r = M.Routing(k, scoring, renormalize=renorm, scale=1.5)
+    run = lambda: M.route_backward(l.cuda(), idx.cuda(), r, d_w.cuda())
+    got = run()
+    want, size = R.route_backward(l.double().numpy(), idx.numpy(), scoring, renorm, 1.5, d_w.numpy())
+    tol = (160 + 4 * _range(l.double().numpy())) * U * size + 1e-37
+    assert np.all(np.abs(got.cpu().double().numpy() - want) <= tol)
+    for _ in range(5):
+        assert torch.equal(got, run())
+
+
 def test_no_tokens():
     l = torch.empty(0, 8, device="cuda")
     r = M.Routing(2)
