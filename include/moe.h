@@ -566,7 +566,8 @@ moe_status_t moe_combine_backward(const moe_bf16_t* d_out, const float* y_perm,
  *   otherwise it overlaps no input. An adapter of smaller rank is padded with zeros.
  *   Sums are fp32; the rank-wide intermediate stays fp32 (or is carried in parts that
  *   together hold at least 16 bits of it for bf16 outputs and 24 for fp32 ones); out is
- *   rounded once.
+ *   rounded once. A row of x with an infinity or NaN, or whose products overflow, gives values
+ *   that are not finite in its own row of out alone.
  *   num_rows >= 0; in_features and out_features positive multiples of 8; rank a multiple of
  *   8 in [8, 128]; 1 <= num_adapters <= 16384; the strides (elements from one row to the next)
  *   multiples of 8, at least the row's length; x, a, b, base and out 16-byte aligned.
