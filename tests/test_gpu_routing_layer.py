@@ -231,3 +231,58 @@ def test_a_tuning_step_of_the_router(scoring, renorm):
     slope = (value(logits.double() + step) - value(logits.double() - step)) / 2e-4
     assert abs(float(slope / want.norm()) - 1) <= 1e-5
     assert dy.shape == y.shape
+
+
+def test_forward_lora_on_another_stream_and_captured():
+    t, h, i, e = 30, 128, 128, 8
+    wr, w1, w3, w2 = [v.cuda() for v in _weights(e, h, i, 21)]
+    x = torch.randn(t, h, device="cuda").bfloat16()
+    adapter = torch.randint(-1, 3, (t,), device="cuda").int()
+    lora = _cuda(_adapters(3, e, h, i, 16, 9))
+    run = lambda **k: M.forward_lora(x, wr, w1, w3, w2, 2, lora, adapter, residual=x, **k)
+    want = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = run(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="thread_local"):
+        got = run()
+    x.copy_(torch.randn(t, h, device="cuda").bfloat16())
+    adapter.copy_(adapter.flip(0))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, run())
+
+
+def test_calls_on_two_streams_at_once():
+    """Each call's scratch is its own: two streams work on different batches side by side."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    r = M.Routing(6, "sigmoid", 8, 4, 2)
+    sets = []
+    for rows in (700, 1000):
+        a, b = (n(5, 16, 512) / 32).bfloat16(), (n(5, 520, 16) / 4).bfloat16()
+        ids = torch.randint(-1, 5, (rows,), device="cuda", generator=g).int()
+        sets.append((n(20000, 64), n(rows, 520), n(rows, 512).bfloat16(), a, b, ids))
+
+    def run(s, **k):
+        logits, base, x, a, b, ids = s
+        idx, w = M.route(logits, r, **k)
+        los = M.router_losses(logits, idx, r, **k)
+        return (idx, w, M.route_backward(logits, idx, r, w, los.counts, los.losses, **k),
+                M.lora_add(base, x, a, b, ids, **k)) + tuple(los)
+
+    want = [run(s) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(10):
+        for j, s in enumerate(sets):
+            got[j].append(run(s, stream=streams[j]))
+    torch.cuda.synchronize()
+    for j in range(2):
+        for out in got[j]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[j]))
