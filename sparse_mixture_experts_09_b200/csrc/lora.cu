@@ -214,15 +214,22 @@ cudaError_t few_rows(const Lora& l, cudaStream_t st) {
 // operations (times the parts of t, below), so mma.sync, whose fragments feed straight
 // from shared memory and whose sums lie in registers beside base, is fast enough:
 // with two thirds of the products left out the expand takes the same time.
-// 4096 rows of 16 adapters, rank 64, 4096 -> 14336 features, fp32: 125 us (plan 6, shrink 18,
-// expand 100, which moves 470 MB at 4.7 TB/s; the floor of all is 82 us).
+// 4096 rows of 16 adapters, rank 64, 4096 -> 14336 features, fp32: 120 us (plan 6, shrink 18,
+// expand 96, which moves 470 MB at 4.9 TB/s; the floor of all is 82 us).
 
 constexpr int kTileRows = 64;
 constexpr int kChunkK = 64;    // features per stage of the shrink
 constexpr int kStages = 4;     // of the shrink
-constexpr int kChunkN = 64;    // columns per step of the expand
-// Steps of the expand in flight beside the one at work: as two blocks an SM have room for.
-__host__ __device__ constexpr int steps_ahead(int out_bytes) { return out_bytes == 4 ? 2 : 3; }
+constexpr int kGroupN = 32;    // columns per step of a group of 4 warps of the expand
+// Of the expand, by the output's bytes and RP: groups of a block, steps in flight beside the one
+// at work, blocks an SM. As the shared memory has room for, at 16 warps an SM.
+struct Expand {
+  int groups, ahead, blocks;
+};
+__host__ __device__ constexpr Expand expand_of(int out_bytes, int RP) {
+  return RP == 128 ? (out_bytes == 4 ? Expand{4, 1, 1} : Expand{2, 2, 2})
+                   : (out_bytes == 4 ? Expand{2, 2, 2} : Expand{2, 3, 2});
+}
 constexpr int kMaxSlices = 8;  // of the features
 
 // In the workspace: the tiles {adapter or -1, first sorted row, rows, 0}, their count, the
@@ -505,15 +512,19 @@ struct Vec<__nv_bfloat16> {
   }
 };
 
-// out = base + t b^T. The tiles' steps of 64 columns, in a row, are cut evenly among as many
-// blocks as run at once; a block takes its steps tile by tile. 8 warps as 4 (16 rows) x 2 (32
-// columns). t's parts times b are exact in fp32; t's fragments stay in registers up to rank 64.
-// base and b come by 16-byte asynchronous copies two or three steps ahead: what has to be in flight
+// out = base + t b^T. The tiles' steps of 32 columns a group, in a row, are cut evenly among as
+// many blocks as run at once; a block takes its steps tile by tile. A group of 4 warps (16 rows
+// each) has its own columns, copies and barrier, so that one group's products run beside
+// another's copies and stores (with one barrier for all 8 warps: 125 us instead of 120 on the
+// case above; with 8 warps an SM at rank 128, 4096 -> 4096 features, bf16 80 instead of 64).
+// t's parts times b are exact in fp32; t's fragments stay in registers up to rank 64.
+// base and b come by 16-byte asynchronous copies one to three steps ahead: what has to be in flight
 // to keep HBM busy (some 50 KB an SM) would not fit the registers beside the sums. b's rows
 // go to shared memory in the order in which a thread's columns of neighbouring 8-wide
 // products are neighbours in out, so that out is written 16 bytes at a time.
 template <typename T, int RP>
-__global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lora l, const Plan p) {
+__global__ void __launch_bounds__(128 * expand_of(sizeof(T), RP).groups, expand_of(sizeof(T), RP).blocks)
+    k_expand_tiles(const Lora l, const Plan p) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(128) uint8_t smem[];
@@ -521,33 +532,38 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
   constexpr int kPitch = RP * 2 + 16;  // odd in 16-byte units: ldmatrix rows fall on distinct banks
   constexpr int kVec = Vec<T>::kN;     // columns of one 16-byte access
   constexpr int kWide = kVec / 2;      // 8-wide products that share it
-  constexpr int kRowBytes = kChunkN * (int)sizeof(T);
+  constexpr Expand kE = expand_of(sizeof(T), RP);
+  constexpr int kThr = 128 * kE.groups, kChunkN = kGroupN * kE.groups;
+  constexpr int kRowBytes = kGroupN * (int)sizeof(T);
   constexpr int kBaseBytes = kTileRows * kRowBytes;
-  constexpr int kStepBytes = kBaseBytes + kChunkN * kPitch;
-  constexpr int kPieces = RP / 8, kAhead = steps_ahead(sizeof(T));
+  constexpr int kStepBytes = kBaseBytes + kGroupN * kPitch;
+  constexpr int kPieces = RP / 8, kAhead = kE.ahead;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int group = warp >> 2, gtid = tid & 127;
   const T* base = static_cast<const T*>(l.base);
   T* out = static_cast<T*>(l.out);
   const int steps = (l.N + kChunkN - 1) / kChunkN;
   const int64_t units = (int64_t)*p.count * steps;
   int64_t unit = units * blockIdx.x / gridDim.x;
   const int64_t end = units * (blockIdx.x + 1) / gridDim.x;
-  const uint32_t t_at = smem_addr(smem), ring = t_at + kParts * kTileRows * kPitch;
-  // this thread's pieces of a step: of base, rows `brow` + kRowStep i at one 16-byte column;
-  // of b, columns (rows of b) q / kPieces at one 16-byte piece
-  constexpr int kRowPieces = kRowBytes / 16, kRowStep = 256 / kRowPieces, kBase = kTileRows / kRowStep;
-  const int brow = tid / kRowPieces, bpiece = tid % kRowPieces;
-  // rows of odd number have the halves of their 128 bytes swapped: two rows' pieces fall on
-  // distinct banks when a quarter of a warp reads them
-  const uint32_t base_dst = ring + brow * kRowBytes + ((bpiece ^ ((brow & 1) << 2)) << 4);
-  constexpr int kB = (kChunkN * kPieces + 255) / 256;
-  const int b_piece = tid % kPieces * 8;
-  const int wr = (warp & 3) * 16, wc = (warp >> 2) * 32;
+  const uint32_t t_at = smem_addr(smem);
+  const uint32_t ring = t_at + kParts * kTileRows * kPitch + group * (kAhead + 1) * kStepBytes;
+  // this thread's pieces of its group's step: of base, rows `brow` + kRowStep i at one 16-byte
+  // column; of b, columns (rows of b) q / kPieces at one 16-byte piece
+  constexpr int kRowPieces = kRowBytes / 16, kRowStep = 128 / kRowPieces, kBase = kTileRows / kRowStep;
+  const int brow = gtid / kRowPieces, bpiece = gtid % kRowPieces;
+  // a quarter of a warp reads 64 bytes of two rows: where a row takes all banks, rows of odd
+  // number have their halves swapped
+  constexpr int kSwap = kRowBytes == 128 ? 4 : 0;
+  const uint32_t base_dst = ring + brow * kRowBytes + ((bpiece ^ (brow & 1) * kSwap) << 4);
+  constexpr int kB = (kGroupN * kPieces + 127) / 128;
+  const int b_piece = gtid % kPieces * 8;
+  const int wr = (warp & 3) * 16, wc = group * kGroupN;
   const int r0 = wr + (lane >> 2), r1 = r0 + 8;
   constexpr bool kKeep = RP <= 64;  // t's fragments stay in registers
   uint32_t kept[kKeep ? RP / 16 : 1][kParts][4];
   const uint32_t t_row = t_at + (wr + (lane & 15)) * kPitch + (lane >> 4) * 16;
-  const uint32_t b_row = kBaseBytes + (wc + (lane & 7) + ((lane >> 4) << 3)) * kPitch + ((lane >> 3) & 1) * 16;
+  const uint32_t b_row = kBaseBytes + ((lane & 7) + ((lane >> 4) << 3)) * kPitch + ((lane >> 3) & 1) * 16;
   constexpr int kGroups = 32 / (8 * kWide);
   while (unit < end) {
     const int tile = (int)(unit / steps), first = (int)(unit - (int64_t)tile * steps);
@@ -558,12 +574,12 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
       if (l.base == l.out) continue;
       const int n0 = first * kChunkN, n1 = last * kChunkN < l.N ? last * kChunkN : l.N;
       const int vecs = (n1 - n0) / kVec, all = vecs * tl.z;
-      for (int i0 = tid; i0 < all; i0 += 256 * 4) {  // four pieces of a thread in flight
+      for (int i0 = tid; i0 < all; i0 += kThr * 4) {  // four pieces of a thread in flight
         uint4 v[4];
         int64_t at[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int i = i0 + 256 * q;
+          const int i = i0 + kThr * q;
           if (i >= all) continue;
           const int64_t r = p.order[tl.y + i / vecs];
           const int n = n0 + i % vecs * kVec;
@@ -572,7 +588,7 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (i0 + 256 * q < all) *reinterpret_cast<uint4*>(out + at[q]) = v[q];
+          if (i0 + kThr * q < all) *reinterpret_cast<uint4*>(out + at[q]) = v[q];
       }
       continue;
     }
@@ -582,7 +598,7 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
     for (int i = 0; i < kBase; ++i) {
       const int r = brow + kRowStep * i;
       row_in[i] = r < tl.z;
-      from[i] = base + (row_in[i] ? (int64_t)p.order[tl.y + r] * l.base_stride : 0) + bpiece * kVec;
+      from[i] = base + (row_in[i] ? (int64_t)p.order[tl.y + r] * l.base_stride : 0) + wc + bpiece * kVec;
     }
     const bool in_row[2] = {r0 < tl.z, r1 < tl.z};
     T* to[2] = {out + (in_row[0] ? (int64_t)p.order[tl.y + r0] * l.out_stride : 0),
@@ -592,16 +608,17 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
       const bool in = s < last;
 #pragma unroll
       for (int i = 0; i < kB; ++i) {
-        const int n = (tid + 256 * i) / kPieces;
-        if (kChunkN * kPieces % 256 && n >= kChunkN) break;
+        const int n = (gtid + 128 * i) / kPieces;
+        if (kGroupN * kPieces % 128 && n >= kGroupN) break;
         // column n = 8 kWide G + 2 kWide c + 2 w + e sits at row 8 kWide G + 8 w + 2 c + e
         const int row = n / (8 * kWide) * (8 * kWide) + (n % (2 * kWide)) / 2 * 8 +
                         (n % (8 * kWide)) / (2 * kWide) * 2 + (n & 1);
-        const bool ok = in && b_piece < l.rank && s * kChunkN + n < l.N;
+        const int col = s * kChunkN + wc + n;
+        const bool ok = in && b_piece < l.rank && col < l.N;
         copy16(ring + stage * kStepBytes + kBaseBytes + row * kPitch + b_piece * 2,
-               ok ? bg + (int64_t)(s * kChunkN + n) * l.rank : l.b, ok);
+               ok ? bg + (int64_t)col * l.rank : l.b, ok);
       }
-      const int col = s * kChunkN + bpiece * kVec;
+      const int col = s * kChunkN + wc + bpiece * kVec;
 #pragma unroll
       for (int i = 0; i < kBase; ++i) {
         const bool ok = in && row_in[i] && col < l.N;
@@ -613,8 +630,8 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
     __syncthreads();  // the tile before is done with the shared memory
     const uint16_t* t = p.t + (int64_t)tl.y * RP;
 #pragma unroll
-    for (int i = 0; i < (kParts * kTileRows * kPieces + 255) / 256; ++i) {
-      const int q = tid + 256 * i, row = q / kPieces;  // rows of all parts, one after another
+    for (int i = 0; i < (kParts * kTileRows * kPieces + kThr - 1) / kThr; ++i) {
+      const int q = tid + kThr * i, row = q / kPieces;  // rows of all parts, one after another
       if (q < kParts * kTileRows * kPieces)
         copy16(t_at + row * kPitch + q % kPieces * 16,
                t + ((int64_t)(row / kTileRows) * (l.R + kTileRows) + row % kTileRows) * RP + q % kPieces * 8, true);
@@ -624,7 +641,10 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
     int stage = 0, col0 = first * kChunkN + wc + (lane & 3) * kVec;
     for (int s = first; s < last; ++s, col0 += kChunkN) {
       copies_wait<kAhead - 1>();
-      __syncthreads();
+      if (s == first)
+        __syncthreads();  // t, which all groups copied
+      else
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
       load(s + kAhead, stage == 0 ? kAhead : stage - 1);
       if constexpr (kKeep) {
         if (s == first) {
@@ -672,9 +692,9 @@ __global__ void __launch_bounds__(256, RP <= 64 ? 2 : 1) k_expand_tiles(const Lo
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!in_row[h]) continue;
-          const int row = h ? r1 : r0, piece = (wc + g * 8 * kWide) / kVec + (lane & 3);
+          const int row = h ? r1 : r0, piece = g * 8 * kWide / kVec + (lane & 3);
           const uint4 was = *reinterpret_cast<const uint4*>(
-              smem + (at - t_at) + row * kRowBytes + ((piece ^ ((row & 1) << 2)) << 4));
+              smem + (at - t_at) + row * kRowBytes + ((piece ^ (row & 1) * kSwap) << 4));
           float f[kVec];
           Vec<T>::get(was, f);
 #pragma unroll
@@ -757,9 +777,10 @@ cudaError_t run_tiles(const Lora& l, const Plan& p, cudaStream_t st) {
                      (unsigned)slices, st, l, p, slices);
   if (e != cudaSuccess) return e;
   const int parts = l.fp32 ? 3 : 2, size = l.fp32 ? 4 : 2;
+  const Expand x = expand_of(size, RP);
   const size_t smem = (size_t)parts * kTileRows * (RP * 2 + 16) +
-                      (size_t)(steps_ahead(size) + 1) * kChunkN * (kTileRows * size + RP * 2 + 16);
-  const dim3 grid((unsigned)(num_sms() * (RP <= 64 ? 2 : 1))), block(256);
+                      (size_t)(x.ahead + 1) * x.groups * kGroupN * (kTileRows * size + RP * 2 + 16);
+  const dim3 grid((unsigned)(num_sms() * x.blocks)), block(128 * x.groups);
   if (l.fp32) {
     e = allow_smem(k_expand_tiles<float, RP>, smem);
     if (e != cudaSuccess) return e;
