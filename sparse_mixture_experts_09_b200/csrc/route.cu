@@ -732,10 +732,10 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
 }
 
 // First pass of the losses: a block's sums of p and of logsumexp^2 and its counts. A lane
-// adds its experts' p over the block's tokens in fp32 (at most a few dozen), the block
+// adds its experts' p over its tokens in fp32 (every 3552nd at 256 experts, 14208th at 64), the block
 // adds its teams' sums in order in double: E + 1 sums and counts. Bound by latency: few bytes
 // and few steps per token, so the next token's loads go out before this one's sums (65521
-// tokens, 64 experts, 6 slots: 17.0 us with the second pass; 18.4 MB, 2.8 us at HBM's rate).
+// tokens, 64 experts, 6 slots: 13.2 us with the second pass; 18.4 MB, 2.8 us at HBM's rate).
 template <typename T, int L, int V, int WARPS>
 __device__ __forceinline__ void block_losses(const Routing& r, const T* __restrict__ logits,
                                              const int32_t* __restrict__ idx,
@@ -866,29 +866,20 @@ __device__ __forceinline__ void finish_losses(const Routing& r, double sum, int3
   }
 }
 
-// Few tokens: one launch, a cluster of 8 blocks of 1024 threads whose first block adds the
-// sums up from their shared memory, in order; no workspace. For 4096 x 8 the device takes 9.2 us
-// against 6.5 with the two passes, but a call 15 us against 19: launches and allocations.
+// The blocks of the grid are one cluster of 8, each with its E + 1 sums and counts in shared
+// memory: the first adds them up in order.
 constexpr int kLossCluster = 8;
-constexpr int64_t kLossTokens = 8192;
 
-template <typename T, int L, int V>
-__global__ void __launch_bounds__(1024)
-    k_losses_few(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
-                 const uint8_t* __restrict__ mask, int vec, float* __restrict__ losses,
-                 int32_t* __restrict__ counts, float* __restrict__ prob_mean) {
-  pdl_trigger();
-  pdl_wait();
-  __shared__ double s_part[L * V + 1];
-  __shared__ int32_t s_parts[L * V + 1];
-  block_losses<T, L, V, 32>(r, logits, idx, mask, vec, s_part, s_parts);
+__device__ __forceinline__ void finish_cluster(const Routing& r, const double* s_sum, const int32_t* s_count,
+                                               float* __restrict__ losses, int32_t* __restrict__ counts,
+                                               float* __restrict__ prob_mean) {
   cluster_sync();
   if (blockIdx.x == 0) {
     double sum = 0.0;
     int32_t count = 0;
     if ((int)threadIdx.x <= r.E) {
-      const uint32_t a = (uint32_t)__cvta_generic_to_shared(&s_part[threadIdx.x]);
-      const uint32_t b = (uint32_t)__cvta_generic_to_shared(&s_parts[threadIdx.x]);
+      const uint32_t a = (uint32_t)__cvta_generic_to_shared(&s_sum[threadIdx.x]);
+      const uint32_t b = (uint32_t)__cvta_generic_to_shared(&s_count[threadIdx.x]);
 #pragma unroll
       for (int w = 0; w < kLossCluster; ++w) {
         uint32_t there;
@@ -907,9 +898,31 @@ __global__ void __launch_bounds__(1024)
   cluster_sync();  // no block leaves while the first reads its sums
 }
 
-// Second pass, one block: thread (e, part) adds every nparts-th block's partials, then
-// the parts are added in order, and one warp's worth of threads the experts. Loads go out
-// eight at a time: with one block there is nothing else to wait beside.
+// Little work: one launch, a cluster of 8 blocks of 1024 threads whose first block adds the sums
+// up from their shared memory; no workspace. It saves a launch and an allocation of the caller's
+// (some 4 us), but has 8 SMs only. Device and whole call, one launch / two passes: 4096 x 8
+// 8.2 / 6.7 and 13.0 / 17.1 us, 8192 x 8 11.9 / 7.3 and 13.0 / 17.1, 4096 x 64 10.7 / 7.6 and
+// 13.2 / 17.3, 8192 x 64 16.5 / 8.1 and 16.8 / 17.3, 1024 x 256 10.2 / 8.1 and 13.0 / 17.1, 4096 x 256
+// 28.1 / 11.4 and 28.7 / 17.1.
+constexpr int64_t kLossTokens = 8192, kLossLogits = 1 << 18;
+
+template <typename T, int L, int V>
+__global__ void __launch_bounds__(1024)
+    k_losses_few(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
+                 const uint8_t* __restrict__ mask, int vec, float* __restrict__ losses,
+                 int32_t* __restrict__ counts, float* __restrict__ prob_mean) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ double s_part[L * V + 1];
+  __shared__ int32_t s_parts[L * V + 1];
+  block_losses<T, L, V, 32>(r, logits, idx, mask, vec, s_part, s_parts);
+  finish_cluster(r, s_part, s_parts, losses, counts, prob_mean);
+}
+
+// Second pass, a cluster of 8 blocks: thread (e, part) adds every (8 nparts)-th block's partials,
+// four loads at a time, then a block's parts are added in pairs, and the blocks and the experts in
+// order. One block alone reads some 60 bytes a cycle: 65521 x 64 17.1 us for both passes instead of
+// 13.2, 16384 x 256 34.9 instead of 15.8; only up to 16 experts is it quicker, by 0.3 us.
 __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks,
                                                      const double* __restrict__ part_sum,
                                                      const int32_t* __restrict__ part_count,
@@ -923,20 +936,21 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
   const int n = r.E + 1;
   const int nparts = 1024 / n;
   const int part = threadIdx.x / n, e = threadIdx.x - part * n;
+  const int step = kLossCluster * nparts;
   double sum = 0.0;
   int32_t count = 0;
   if (part < nparts) {
-    for (int b = part; b < blocks; b += 8 * nparts) {
-      double s[8];
-      int32_t c[8];
+    for (int b = (int)blockIdx.x * nparts + part; b < blocks; b += 4 * step) {
+      double s[4];
+      int32_t c[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int at = b + i * nparts;
+      for (int i = 0; i < 4; ++i) {
+        const int at = b + i * step;
         s[i] = at < blocks ? part_sum[(int64_t)at * n + e] : 0.0;
         c[i] = at < blocks ? part_count[(int64_t)at * n + e] : 0;
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         sum += s[i];
         count += c[i];
       }
@@ -956,8 +970,7 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
     live = half;
     __syncthreads();
   }
-  const bool mine = threadIdx.x < n;
-  finish_losses(r, mine ? s_sum[threadIdx.x] : 0.0, mine ? s_count[threadIdx.x] : 0, losses, counts, prob_mean);
+  finish_cluster(r, s_sum, s_count, losses, counts, prob_mean);
 }
 
 // Gradient in the logits. With g_j = weight_scale * d_topk_w[j], and for the losses
@@ -1218,7 +1231,9 @@ cudaError_t launch_route(const Routing& r, const void* logits, const float* bias
 }
 
 namespace {
-bool few_for_losses(const Routing& r) { return r.T <= kLossTokens && r.E <= 256; }
+bool few_for_losses(const Routing& r) {
+  return r.E <= 256 && r.T <= kLossTokens && r.T * r.E <= kLossLogits;
+}
 }  // namespace
 
 int router_loss_blocks(const Routing& r) {
@@ -1268,8 +1283,8 @@ cudaError_t launch_router_losses(const Routing& r, const void* logits, const int
     });
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(k_losses_end, dim3(1), dim3(1024), 0, st, r, blocks, part_sum, part_count,
-                    losses, counts, prob_mean);
+  return launch_cluster(k_losses_end, kLossCluster, 1024, 0, kLossCluster, st, r, blocks, part_sum,
+                        part_count, losses, counts, prob_mean);
 }
 
 cudaError_t launch_route_backward(const Routing& r, const void* logits, const int32_t* idx,

@@ -211,6 +211,13 @@ def test_losses(t, e, k, scoring):
                     assert abs(got.losses[1].item() - want[0][1]) <= (32 + _range(ln)) * U * size
 
 
+@pytest.mark.parametrize("t,e,k", [(4096, 64, 6), (4097, 64, 6), (1024, 256, 8), (1025, 256, 8), (8192, 32, 4), (9000, 17, 4),
+                                   (600, 512, 8), (30000, 128, 8)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_losses_around_the_change_of_form(t, e, k, scoring):
+    test_losses(t, e, k, scoring)
+
+
 @pytest.mark.parametrize("t,e,k", SHAPES)
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
