@@ -415,6 +415,7 @@ __global__ void __launch_bounds__(128) k_shrink_tiles(const Lora l, const Plan p
     copies_wait<kStages - 2>();
     __syncthreads();
     load(c + kStages - 1, (c - c0 + kStages - 1) % kStages);
+    if (warp * 16 >= tl.z) continue;  // none of the tile's rows
     const uint32_t xt = base + ((c - c0) % kStages) * kStageBytes, at = xt + kTileRows * 128;
     float acc[RP / 8][4];
 #pragma unroll
@@ -715,15 +716,18 @@ int rank_pad(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ?
 
 // Whether the rows go by tiles. A row on its own streams its adapter again for every row; a
 // tile costs as much for one row as for 64, and the sorting and two more launches some 8 us.
-// Device times, rows / tiles: 64 rows of 4 adapters, rank 64, 4096 -> 14336 features 27 / 20 us,
-// of 64 adapters 36 / 67; 128 rows of 8 adapters, rank 16, 4096 -> 4096 11 / 14 us; 256 rows of 8
-// adapters 20 / 15, of 256 adapters 23 / 41; 192 rows of 192 adapters 17 / 35. How many adapters a
-// batch uses is not known here, only how many there are: from 256 rows on, and for heavy
-// adapters from 128, the tiles lose less in their worst case than they gain in their best.
+// Device times, rows / tiles, where the rows fall on all of the adapters: 64 rows of 4 adapters,
+// rank 64, 4096 -> 14336 features 27 / 20 us, of 64 38 / 60. 4096 -> 4096 features, rank 16: 128 rows
+// of 2 adapters 11.5 / 12, of 16 11.5 / 15; 256 rows of 16 20 / 16, of 64 20 / 22, of 256 23 / 39, of 1024
+// 25 / 51; 512 rows of 64 36 / 23, of 256 44 / 53; rank 64: 128 rows of 16 34 / 22, of 256 45 / 52.
+// How many adapters a batch uses is not known here, only how many there are: where the better
+// form depends on that, the one whose worst case loses less is taken.
 bool use_tiles(const Lora& l) {
   const bool light = l.R * (int64_t)l.rank * (l.H + l.N) * 2 < (int64_t)64 << 20;
   if (l.R < 128) return !light && l.R >= 12 * (int64_t)l.G;
+  if (l.R < 160) return !light;
   if (l.R < 256) return !light || l.R >= 8 * (int64_t)l.G;
+  if (l.R < 512 && l.rank <= 16) return l.R >= 4 * (int64_t)l.G;
   return true;
 }
 

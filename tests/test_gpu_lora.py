@@ -78,6 +78,14 @@ def test_against_fp64(r, h, n, rank, ad, dtype, order):
     _check(_case(r, h, n, rank, ad, dtype, order, r + n))
 
 
+@pytest.mark.parametrize("r,h,n,rank,ad", [(159, 264, 200, 16, 2), (160, 264, 200, 16, 20), (160, 264, 200, 16, 21), (300, 136, 264, 8, 200),
+                                           (511, 72, 104, 16, 128), (512, 72, 104, 16, 400), (300, 136, 264, 24, 200),
+                                           (900, 200, 1032, 128, 3), (260, 328, 40, 128, 17), (400, 96, 168, 104, 9)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_around_the_change_of_form(r, h, n, rank, ad, dtype):
+    _check(_case(r, h, n, rank, ad, dtype, "mixed", r + ad))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("r", [5, 190, 1100])
 def test_in_place_no_scale_and_into_out(dtype, r):
