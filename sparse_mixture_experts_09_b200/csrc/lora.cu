@@ -248,33 +248,43 @@ __host__ __device__ inline int64_t max_tiles(int64_t R, int G) {
 }
 
 // Counting sort of the rows by adapter, one block: rows without an adapter form group G.
-// Lanes of a warp with the same adapter add once (runs of a request are the common case).
+// A warp of one adapter adds once (runs of a request are the common case). A row's place in its
+// group is known from the counting; later rounds leave it where t will be. 4096 rows 6 us, 7 where
+// 64 adapters alternate (12 with the lanes matched, and the places found by a second count).
 __global__ void __launch_bounds__(1024) k_plan(const Lora l, Plan p) {
   pdl_trigger();
   pdl_wait();
-  extern __shared__ int32_t s_cursor[];  // [G + 1] counts, then each group's next position
+  extern __shared__ int32_t s_cursor[];  // [G + 1] counts, then each group's start
   __shared__ int32_t s_rows[32], s_tiles[32];
   const int groups = l.G + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int g = threadIdx.x; g < groups; g += 1024) s_cursor[g] = 0;
   __syncthreads();
-  constexpr int kKept = 4;  // rounds whose groups stay in registers
-  int kept[kKept];
-  const auto group_of = [&](int64_t r) {
+  constexpr int kKept = 4;  // rounds whose groups and places stay in registers
+  int kept[kKept], place[kKept];
+  int32_t* places = reinterpret_cast<int32_t*>(p.t);  // [R]: t has 64 bytes a row or more
+  const auto group_of = [&](int r) {  // R is at most 2^24
     if (r >= l.R) return -1;
     const int g = l.adapter[r];
     return g >= 0 && g < l.G ? g : l.G;
   };
 #pragma unroll
   for (int i = 0; i < kKept; ++i) kept[i] = group_of(i * 1024 + threadIdx.x);
-  const int64_t rounds = (l.R + 1023) / 1024;
+  const int rounds = (int)((l.R + 1023) / 1024);
   const auto count = [&](int g) {
-    const unsigned same = __match_any_sync(0xffffffffu, g);
-    if (g >= 0 && lane == __ffs(same) - 1) atomicAdd(&s_cursor[g], __popc(same));
+    if (!__all_sync(0xffffffffu, g == __shfl_sync(0xffffffffu, g, 0)))
+      return g >= 0 ? atomicAdd(&s_cursor[g], 1) : 0;
+    int at = 0;
+    if (g >= 0 && lane == 0) at = atomicAdd(&s_cursor[g], 32);
+    return __shfl_sync(0xffffffffu, at, 0) + lane;
   };
 #pragma unroll
   for (int i = 0; i < kKept; ++i)
-    if (i < rounds) count(kept[i]);
-  for (int64_t i = kKept; i < rounds; ++i) count(group_of(i * 1024 + threadIdx.x));
+    if (i < rounds) place[i] = count(kept[i]);
+  for (int i = kKept; i < rounds; ++i) {
+    const int r = i * 1024 + threadIdx.x;
+    const int at = count(group_of(r));
+    if (r < l.R) places[r] = at;
+  }
   __syncthreads();
   // exclusive prefixes of rows and tiles over the groups: `per` neighbouring groups a thread
   const int per = (groups + 1023) / 1024;
@@ -309,25 +319,18 @@ __global__ void __launch_bounds__(1024) k_plan(const Lora l, Plan p) {
   if (threadIdx.x == 1023) *p.count = tile_at + tiles;
   for (int g = g0; g < g1; ++g) {
     const int n = s_cursor[g];
-    s_cursor[g] = row_at;
+    s_cursor[g] = row_at;  // where the group starts
     for (int i = 0; i < n; i += kTileRows)
       p.tiles[tile_at++] = make_int4(g < l.G ? g : -1, row_at + i, n - i < kTileRows ? n - i : kTileRows, 0);
     row_at += n;
   }
   __syncthreads();
-  const auto place = [&](int64_t r, int g) {
-    const unsigned same = __match_any_sync(0xffffffffu, g);
-    int at = 0;
-    if (g >= 0 && lane == __ffs(same) - 1) at = atomicAdd(&s_cursor[g], __popc(same));
-    at = __shfl_sync(0xffffffffu, at, __ffs(same) - 1);
-    if (g >= 0) p.order[at + __popc(same & ((1u << lane) - 1u))] = (int32_t)r;
-  };
 #pragma unroll
   for (int i = 0; i < kKept; ++i)
-    if (i < rounds) place(i * 1024 + threadIdx.x, kept[i]);
-  for (int64_t i = kKept; i < rounds; ++i) {
-    const int64_t r = i * 1024 + threadIdx.x;
-    place(r, group_of(r));
+    if (kept[i] >= 0) p.order[s_cursor[kept[i]] + place[i]] = i * 1024 + threadIdx.x;
+  for (int i = kKept; i < rounds; ++i) {
+    const int r = i * 1024 + threadIdx.x;
+    if (r < l.R) p.order[s_cursor[group_of(r)] + places[r]] = r;
   }
 }
 
