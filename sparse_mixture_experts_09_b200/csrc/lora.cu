@@ -251,7 +251,7 @@ __host__ __device__ inline int64_t max_tiles(int64_t R, int G) {
 // A warp of one adapter adds once (runs of a request are the common case). A row's place in its
 // group is known from the counting; later rounds leave it where t will be. 4096 rows 6 us, 7 where
 // 64 adapters alternate (12 with the lanes matched, and the places found by a second count).
-__global__ void __launch_bounds__(1024) k_plan(const Lora l, Plan p) {
+__global__ void __launch_bounds__(1024, 1) k_plan(const Lora l, Plan p) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ int32_t s_cursor[];  // [G + 1] counts, then each group's start
