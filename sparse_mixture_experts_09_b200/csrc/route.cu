@@ -984,7 +984,7 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
 //   z: 2 d1 / N * logsumexp * softmax_e.
 // A slot's term crosses from its lane to its expert's through shared memory. Bound by
 // instructions (580 a token at 256 experts, 57% of the issue slots): 16384 x 256 with sigmoid scores
-// and losses 16.9 us (34.6 MB: 5.3 us at HBM's rate), 4096 x 8 4.4 us.
+// and losses 17.1 us (34.6 MB: 5.3 us at HBM's rate), 4096 x 8 4.6 us.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
     k_route_bwd(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
