@@ -197,7 +197,9 @@ __device__ __forceinline__ double sigmoid_in_double(float l) {
 
 // The groups that stay, as a ballot (bit base + g * lanes for group g). A value may be off by
 // tol + 2 u |value|; `close` is set where the last group that stays and the first that goes
-// are not further apart than that allows. A group's one or two best: its lanes take their own
+// are not further apart than that allows. With no bias and one expert a group the values are the
+// logits themselves, which fp32 compares exactly; they are not judged again by scores, which are equal
+// for different logits where a sigmoid saturates. A group's one or two best: its lanes take their own
 // values, or every lanes-th from shared memory, and merge their pairs. Close groups of
 // sigmoid scores are judged again by the values in double of those experts that can be
 // among their best.
@@ -239,6 +241,8 @@ __device__ __forceinline__ unsigned open_groups(const Routing& r, const Team<L>&
     above += other > mine || (other == mine && j < g);
   }
   const bool in = above < r.topk_groups;
+  close = false;
+  if (!bias && r.group_top == 1) return __ballot_sync(team.mask, in);  // logits: exact
   const bool real = g < r.groups;
   // what a group's value may be off by: its terms' bounds and their sum's rounding
   const float off = real ? 2 * tol + 0x1p-22f * (fabsf(m1) + (r.group_top == 2 ? fabsf(m2) : 0.f)) : 0.f;
@@ -642,7 +646,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
     if (r.groups > 1) {
       bool near = false;
       stay = open_groups(r, team, groups, row, bias, c, tol, reinterpret_cast<float*>(shared), near);
-      if (scores && near) return false;
+      if (near) return false;
     }
     if (bias) {
 #pragma unroll
