@@ -1045,11 +1045,11 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
         ls = clean(logit_at(row + my_e));
       }
     }
-    float p[V], dl[V], lse = 0.f;
+    float p[V], dl[V], lse = 0.f, top = 0.f, inv = 0.f;
     const bool need_p = losses || (d_w && !r.sigmoid && !r.renorm);
     if (need_p) {
       mx = team.max(mx);
-      const float top = mx > -INFINITY ? mx : 0.f;  // exp(l - top) is 0 where no expert has a score
+      top = mx > -INFINITY ? mx : 0.f;  // exp(l - top) is 0 where no expert has a score
       float sum = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -1058,7 +1058,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
       }
       sum = team.sum(sum);
       lse = sum > 0.f ? top + logf(sum) : 0.f;
-      const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+      inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) p[v] *= inv;
     }
@@ -1108,7 +1108,8 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
         term = u * rest * g;
       } else {
         float gp = 0.f;
-        if (my_e >= 0 && ls > -INFINITY) u = fast_exp2(kLog2e * (ls - lse));
+        // as p is formed: lse, once rounded, would bring in an error of |lse| 2^-24
+        if (my_e >= 0) u = fast_exp2(kLog2e * (ls - top)) * inv;
         gp = team.sum(g * u);  // every lane needs it
         term = u * g;
 #pragma unroll
