@@ -118,10 +118,12 @@ __global__ void __launch_bounds__(kThreads) k_combine_bwd(const CombineBwd c, in
 cudaError_t launch_combine_bwd(const CombineBwd& c, cudaStream_t st) {
   const int64_t cap = (int64_t)num_sms() * 8;
   const int token_blocks = (int)(c.T < 4 * cap ? c.T : 4 * cap);
-  // T * k of `rows` rows are named; the rest bounds the zeroing blocks
-  int64_t zero_blocks = c.dy ? c.rows - c.T * c.k : 0;
-  if (zero_blocks > cap) zero_blocks = cap;
-  if (c.dy && c.rows > 0 && zero_blocks < 1) zero_blocks = 1;  // slots may name no row
+  // T * k of `rows` rows are named, or fewer where slots name no row; the rest bounds the zeroing blocks
+  int64_t zero_blocks = 0;
+  if (c.dy && c.rows > 0) {
+    const int64_t unnamed = c.rows - c.T * c.k;
+    zero_blocks = unnamed > cap ? cap : unnamed > 1 ? unnamed : 1;
+  }
   const int64_t blocks = token_blocks + zero_blocks;
   if (blocks == 0) return cudaSuccess;
   const dim3 grid((unsigned)blocks), block(kThreads);
