@@ -1098,7 +1098,7 @@ def forward_lora(x, w_router, w1, w3, w2, k: int, adapters: LoraExperts, adapter
         count = count or a.shape[0]
         if a.shape[0] != count or tuple(b.shape) != (count, e, n_out, a.shape[2]):
             raise ValueError(f"b{name} must be [{count}, {e}, {n_out}, {a.shape[2]}], got {tuple(b.shape)}")
-        pairs[name] = (a.reshape(count * e, a.shape[2], n_in), b.reshape(count * e, n_out, a.shape[2]))
+        pairs[name] = (a, b)
     if not pairs:
         raise ValueError("adapters holds no pair")
     _sized("scale", adapters.scale, count)
@@ -1121,7 +1121,9 @@ def forward_lora(x, w_router, w1, w3, w2, k: int, adapters: LoraExperts, adapter
             y = torch.empty(rows, n_out, dtype=torch.float32, device=x.device)
             expert_down(rows_in, perm["offsets"], weights, t, k, ws, y=y, weight_layout=weight_layout)
             if name in pairs:
-                lora_add(y, rows_in[:rows], *pairs[name], ids, scale, out=y)
+                # where adapters and experts cannot be merged (a shard's experts) this copies: on the call's stream
+                a, b = (p.reshape(count * e, *p.shape[2:]) for p in pairs[name])
+                lora_add(y, rows_in[:rows], a, b, ids, scale, out=y)
             return y
 
         gate, up = project(perm["x_perm"], w1, i, "1"), project(perm["x_perm"], w3, i, "3")
