@@ -766,11 +766,13 @@ Plan plan_at(const Lora& l, void* ws, size_t* end) {
   return p;
 }
 
-// A block's shared memory above 48 KB has to be asked for (1 KB is left to static arrays).
+// A block's shared memory above 48 KB has to be asked for (1 KB is left to static arrays). The limit
+// belongs to the kernel, not to the call, so calls of one kernel all ask for `most`, the most that it
+// ever takes: no host thread lowers it between another's request and its launch.
 template <typename F>
-cudaError_t allow_smem(F* kernel, size_t bytes) {
+cudaError_t allow_smem(F* kernel, size_t bytes, size_t most) {
   if (bytes <= 47 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
 }
 
 template <int RP>
@@ -778,7 +780,7 @@ cudaError_t run_tiles(const Lora& l, const Plan& p, cudaStream_t st) {
   const int slices = feature_slices(l);
   const int64_t tiles = max_tiles(l.R, l.G);
   const size_t shrink_smem = (size_t)kStages * (kTileRows + RP) * kChunkK * 2;
-  cudaError_t e = allow_smem(k_shrink_tiles<RP>, shrink_smem);
+  cudaError_t e = allow_smem(k_shrink_tiles<RP>, shrink_smem, shrink_smem);
   if (e != cudaSuccess) return e;
   e = launch_cluster(k_shrink_tiles<RP>, (unsigned)(tiles * slices), 128, shrink_smem,
                      (unsigned)slices, st, l, p, slices);
@@ -789,11 +791,11 @@ cudaError_t run_tiles(const Lora& l, const Plan& p, cudaStream_t st) {
                       (size_t)(x.ahead + 1) * x.groups * kGroupN * (kTileRows * size + RP * 2 + 16);
   const dim3 grid((unsigned)(num_sms() * x.blocks)), block(128 * x.groups);
   if (l.fp32) {
-    e = allow_smem(k_expand_tiles<float, RP>, smem);
+    e = allow_smem(k_expand_tiles<float, RP>, smem, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(k_expand_tiles<float, RP>, grid, block, smem, st, l, p);
   }
-  e = allow_smem(k_expand_tiles<__nv_bfloat16, RP>, smem);
+  e = allow_smem(k_expand_tiles<__nv_bfloat16, RP>, smem, smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_expand_tiles<__nv_bfloat16, RP>, grid, block, smem, st, l, p);
 }
@@ -812,7 +814,7 @@ cudaError_t launch_lora(const Lora& l, void* ws, cudaStream_t st) {
     size_t end = 0;
     const Plan p = plan_at(l, ws, &end);
     const size_t smem = (size_t)(l.G + 1) * 4;
-    cudaError_t e = allow_smem(k_plan, smem);
+    cudaError_t e = allow_smem(k_plan, smem, (size_t)(kLoraMaxAdapters + 1) * 4);
     if (e != cudaSuccess) return e;
     e = launch_pdl(k_plan, dim3(1), dim3(1024), smem, st, l, p);
     if (e != cudaSuccess) return e;

@@ -217,6 +217,7 @@ struct CombineBwd {
 cudaError_t launch_combine_bwd(const CombineBwd& c, cudaStream_t st);
 
 // Low-rank adapters beside a shared projection (lora.cu).
+constexpr int kLoraMaxAdapters = 16384;
 struct Lora {
   int64_t R, x_stride, base_stride, out_stride;
   int H, N, rank, G;

@@ -127,9 +127,9 @@ moe_status_t check_lora(const moe_lora_t* in, Lora* out) {
                      "(got %d and %d)", in->in_features, in->out_features);
   if (in->rank < 8 || in->rank > 128 || in->rank % 8)
     return fail_with(MOE_ERR_UNSUPPORTED, "rank must be a multiple of 8 in [8, 128] (got %d)", in->rank);
-  if (in->num_adapters < 1 || in->num_adapters > 16384)
-    return fail_with(MOE_ERR_UNSUPPORTED, "num_adapters must be in [1, 16384] (got %d)",
-                     in->num_adapters);
+  if (in->num_adapters < 1 || in->num_adapters > kLoraMaxAdapters)
+    return fail_with(MOE_ERR_UNSUPPORTED, "num_adapters must be in [1, %d] (got %d)",
+                     kLoraMaxAdapters, in->num_adapters);
   if (in->x_stride < in->in_features || in->x_stride % 8 || in->base_stride < in->out_features ||
       in->base_stride % 8 || in->out_stride < in->out_features || in->out_stride % 8)
     return fail_with(MOE_ERR_INVALID_ARG,
@@ -310,10 +310,10 @@ moe_status_t moe_lora_rows(const int32_t* token_of_row, const int32_t* expert_of
     return fail_with(MOE_ERR_INVALID_ARG, "num_tokens and num_rows must be in [0, 2^31)");
   if (num_experts < 1 || num_experts > 512)
     return fail_with(MOE_ERR_UNSUPPORTED, "num_experts must be in [1, 512] (got %d)", num_experts);
-  if (num_adapters < 1 || num_adapters > 16384 / num_experts)
+  if (num_adapters < 1 || num_adapters > kLoraMaxAdapters / num_experts)
     return fail_with(MOE_ERR_UNSUPPORTED,
-                     "num_adapters must be >= 1 and num_adapters * num_experts <= 16384 (got %d)",
-                     num_adapters);
+                     "num_adapters must be >= 1 and num_adapters * num_experts <= %d (got %d)",
+                     kLoraMaxAdapters, num_adapters);
   if (num_rows == 0) return MOE_OK;
   MOE_TRY(check_aligned(token_of_row, "token_of_row", 4, false));
   MOE_TRY(check_aligned(expert_offsets, "expert_offsets", 4, false));
