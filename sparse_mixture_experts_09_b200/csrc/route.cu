@@ -43,6 +43,14 @@ __device__ __forceinline__ void sigmoid_pair(float l, float& s, float& rest) {
   rest = l >= 0.f ? small : big;
 }
 
+// Below -32 a sigmoid is an exponential to 2^-46, and the shares s / sum s do not change with a common
+// offset of the logits: where the largest logit `top` is below, it is moved to -32 for them, so
+// that none is lost to the subnormals. Below kNoScore the routing's own sigmoids (in double) are 0.
+constexpr float kNoScore = -709.f;
+__device__ __forceinline__ float share_shift(float top) {
+  return top < -32.f && top > kNoScore ? top + 32.f : 0.f;
+}
+
 // NaN -> -inf, +inf -> the largest float: exp(l - max) is then 0 or finite everywhere.
 __device__ __forceinline__ float clean(float l) { return fminf(fmaxf(l, -INFINITY), FLT_MAX); }
 
@@ -793,11 +801,12 @@ __device__ __forceinline__ void block_losses(const Routing& r, const T* __restri
     sum = team.sum(sum);
     const float lse = sum > 0.f ? top + logf(sum) : 0.f;  // no expert has a score: no z term
     if (r.sigmoid) {
+      const float shift = share_shift(top);
       sum = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float rest;
-        sigmoid_pair(l[v], x[v], rest);
+        sigmoid_pair(l[v] - shift, x[v], rest);
         sum += x[v];
       }
       sum = team.sum(sum);
@@ -982,7 +991,8 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
 //   softmax, renormalised: u = softmax over the chosen logits; dl_j = u_j (g_j - sum g u)
 //     (the sum over all experts cancels, and with it the loss of digits in it);
 //   softmax: dl_e = p_e ([chosen] g_e - sum g p);
-//   sigmoid, renormalised: dl_j = (1 - s_j) u_j (g_j - sum g u), u = s / sum of chosen s;
+//   sigmoid, renormalised: dl_j = (1 - s_j) u_j (g_j - sum g u), u = s / sum of chosen s
+//     (u and the balance's s / sum s of very negative logits from logits moved up);
 //   sigmoid: dl_j = s_j (1 - s_j) g_j;
 //   balance: softmax p_e (c_e - sum c p); sigmoid s_e (1 - s_e) (c_e - sum c p) / sum s;
 //   z: 2 d1 / N * logsumexp * softmax_e.
@@ -1003,6 +1013,7 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
   float* slots = s_slots[threadIdx.x / L];
   int pairs = 1;  // lanes up to the next power of two of k
   while (pairs < r.k) pairs *= 2;
+  const unsigned slot_mask = (pairs == 32 ? 0xffffffffu : (1u << pairs) - 1u) << team.base;
   // over the slots' lanes (the others get what theirs amount to)
   const auto slots_sum = [&](float v) {
     for (int o = pairs >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(team.mask, v, o);
@@ -1067,21 +1078,22 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
     if (losses) {
       float cs = 0.f;
       if (r.sigmoid) {
+        const float shift = share_shift(top);
         float s[V], sum = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           float rest;
-          sigmoid_pair(l[v], s[v], rest);
+          sigmoid_pair(l[v] - shift, s[v], rest);
           sum += s[v];
           cs += c[v] * s[v];
           dl[v] = s[v] * rest;
         }
         sum = team.sum(sum);
-        const float inv = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
-        cs = team.sum(cs) * inv;
+        const float over = sum > 0.f ? __fdividef(1.f, sum) : 0.f;
+        cs = team.sum(cs) * over;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          dl[v] = dl[v] * ((c[v] - cs) * inv) + zc * lse * p[v];
+          dl[v] = dl[v] * ((c[v] - cs) * over) + zc * lse * p[v];
         }
       } else {
 #pragma unroll
@@ -1101,7 +1113,14 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
       }
       float term = 0.f;  // what slot `rank` adds to its expert
       if (r.renorm) {
-        const float sum = slots_sum(u);
+        float sum = slots_sum(u);
+        if (r.sigmoid && sum < 0x1p-46f && team.rank < pairs) {  // all of the slots' lanes, or none
+          float most = ls;
+          for (int o = pairs >> 1; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(slot_mask, most, o));
+          u = most > kNoScore ? fast_exp2(kLog2e * (ls - most)) : 0.f;
+          sum = u;
+          for (int o = pairs >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(slot_mask, sum, o);
+        }
         u = sum > 0.f ? __fdividef(u, sum) : 0.f;
         term = u * (g - slots_sum(g * u)) * rest;
       } else if (r.sigmoid) {

@@ -1,7 +1,8 @@
-"""The losses and the gradient in the logits where the logits have a common offset: against
-fp64, with the bounds of the other gradient tests (u = 2^-24, R the largest |l - max l| that has
-weight): 128 + 4 R u of the terms' magnitudes for the gradient, 96 + 2 R u for the mean
-probabilities."""
+"""The losses and the gradient in the logits where the logits have a common offset, or are so
+negative that a sigmoid is below fp32's range: against fp64, with the bounds of the other gradient
+tests (u = 2^-24, R the largest |l - max l| that has weight): 128 + 4 R u of the terms' magnitudes
+for the gradient, 96 + 2 R u for the mean probabilities. A sigmoid of a logit of -32 to -64 adds half a
+step of its exponential's argument to what those count, 22 u; its share of a sum twice that."""
 import numpy as np
 import pytest
 import torch
@@ -47,3 +48,20 @@ def test_softmax_with_an_offset(e, k, renorm, offset):
     l = torch.randn(T, e, generator=torch.Generator().manual_seed(e))
     step = max(2.0 ** -20, abs(offset) * 2.0 ** -23)
     _compare(torch.round(l / step) * step + offset, k, "softmax", renorm)
+
+
+@pytest.mark.parametrize("e,k", [(8, 2), (16, 8), (64, 6), (100, 12), (256, 8), (512, 32)])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("offset", [-30.0, -60.0, -84.0, -88.0, -110.0, -650.0, 60.0])
+def test_sigmoid_with_an_offset(e, k, renorm, offset):
+    _compare(torch.randn(T, e, generator=torch.Generator().manual_seed(e)) + offset, k, "sigmoid", renorm)
+
+
+@pytest.mark.parametrize("e,k", [(8, 3), (64, 6), (256, 8)])
+def test_sigmoid_rows_of_every_size(e, k):
+    """Tokens of all offsets in one call, a single ordinary logit among very negative ones."""
+    g = torch.Generator().manual_seed(e)
+    l = torch.randn(T, e, generator=g) - 300 * torch.rand(T, 1, generator=g)
+    l[::5, 1] = 0.5
+    _compare(l, k, "sigmoid", True)
+    _compare(l, k, "sigmoid", False)
