@@ -458,8 +458,9 @@ moe_status_t moe_combine_peer(const float* const* y_bases, int world, int64_t y_
  * their logits.
  * A NaN logit counts as -infinity, and a logit of +infinity as the largest float. An
  * expert of logit -infinity has score 0; a NaN select_bias makes its expert's c
- * -infinity. Experts whose c is -infinity come last, lower index first. Slots whose
- * scores sum to 0 have weight 0 where renormalised. */
+ * -infinity. Experts whose c is -infinity come last, lower index first. A group with a c of
+ * +infinity has the value +infinity. Scores are formed in double: a sigmoid below -709 is 0. Slots
+ * whose scores sum to 0 have weight 0 where renormalised. */
 #define MOE_SCORING_SOFTMAX 0
 #define MOE_SCORING_SIGMOID 1
 

@@ -57,8 +57,8 @@ def route(logits, k: int, scoring="softmax", num_groups=1, topk_groups=1, group_
         if num_groups > 1:
             value = []
             for g in range(num_groups):
-                v = np.sort(by_group[t, g * gs:(g + 1) * gs])[::-1]
-                value.append(v[:group_top].sum())
+                v = np.sort(by_group[t, g * gs:(g + 1) * gs])[::-1][:group_top]
+                value.append(np.inf if np.isposinf(v).any() else v.sum())
             free = np.ones(num_groups, dtype=bool)
             for _ in range(topk_groups):
                 free[_first_largest(value, free)] = False

@@ -285,7 +285,8 @@ __device__ __forceinline__ unsigned open_groups(const Routing& r, const Team<L>&
     d2 = fmax(fmax(d2, o2), fmin(d1, o1));
     d1 = fmax(d1, o1);
   }
-  const double exact = r.group_top == 2 ? d1 + d2 : d1;
+  // a group with a value of +infinity has that, whatever the other is
+  const double exact = r.group_top == 2 && d1 < INFINITY ? d1 + d2 : d1;
   above = 0;
 #pragma unroll 1
   for (int j = 0; j < r.groups; ++j) {
@@ -529,7 +530,7 @@ __device__ __noinline__ void route_in_double(const Routing r, const T* row, cons
             at = i;
           }
         }
-        value += best;
+        if (value < INFINITY) value += best;  // +infinity (the first, if any) stays, whatever follows
         taken[at >> 5] |= 1u << (at & 31);
       }
     }
