@@ -464,7 +464,7 @@ moe_status_t moe_combine_peer(const float* const* y_bases, int world, int64_t y_
 #define MOE_SCORING_SOFTMAX 0
 #define MOE_SCORING_SIGMOID 1
 
-/* Sizes: num_tokens >= 0 (0: nothing is launched), 1 <= num_experts <= 512,
+/* Sizes: 0 <= num_tokens <= 2^30 (0: nothing is launched), 1 <= num_experts <= 512,
  * 1 <= num_experts_per_tok <= min(32, topk_groups * E / num_groups), num_groups <= 32
  * divides num_experts, 1 <= topk_groups <= num_groups, 1 <= group_top <= E / num_groups
  * (one group: topk_groups = group_top = 1). logits_bf16: 0 logits are fp32, 1 bf16.
@@ -538,8 +538,8 @@ moe_status_t moe_route_backward(const moe_routing_t* routing, const void* logits
 /* Gradient of moe_combine (the residual's is d_out itself):
  *   dy_perm[row_of[t,j]] = topk_w[t,j] * d_out[t]   (fp32; one rounding)
  *   d_topk_w[t,j]        = sum_h d_out[t,h] * y_perm[row_of[t,j],h]   (fp32 sum)
- * and zero in every row of dy_perm that no slot names: the groups' pad rows and the rows
- * past the last group.
+ * and zero in every row of dy_perm that no slot names: the groups' pad rows, the rows past the
+ * last group, and routed rows whose slot was taken out (its row_of set outside the buffer).
  *   d_out [T, hidden] bf16; y_perm [num_rows, hidden] fp32; row_of [T, k] int32, distinct
  *   rows (a row outside [0, num_rows) is no slot: nothing is written for it and its
  *   d_topk_w is 0); topk_w [T, k] fp32; expert_counts [E] and expert_offsets [E + 1] int32 as
@@ -547,8 +547,8 @@ moe_status_t moe_route_backward(const moe_routing_t* routing, const void* logits
  *   dy_perm [num_rows, hidden] fp32 out, nullable (then topk_w, expert_counts and
  *   expert_offsets are not read and may be NULL); d_topk_w [T, k] fp32 out, nullable (then
  *   y_perm is not read and may be NULL).
- *   num_tokens >= 0, 1 <= k <= 8, hidden a positive multiple of 8, 1 <= num_experts <= 512,
- *   num_rows >= 0. */
+ *   num_tokens >= 0, num_tokens * k <= 2^30, 1 <= k <= 8, hidden a positive multiple of 8,
+ *   1 <= num_experts <= 512, 0 <= num_rows < 2^31. */
 moe_status_t moe_combine_backward(const moe_bf16_t* d_out, const float* y_perm,
                                   const int32_t* row_of, const float* topk_w,
                                   const int32_t* expert_counts, const int32_t* expert_offsets,
@@ -569,9 +569,9 @@ moe_status_t moe_combine_backward(const moe_bf16_t* d_out, const float* y_perm,
  *   together hold at least 16 bits of it for bf16 outputs and 24 for fp32 ones); out is
  *   rounded once. A row of x with an infinity or NaN, or whose products overflow, gives values
  *   that are not finite in its own row of out alone.
- *   num_rows >= 0; in_features and out_features positive multiples of 8; rank a multiple of
- *   8 in [8, 128]; 1 <= num_adapters <= 16384; the strides (elements from one row to the next)
- *   multiples of 8, at least the row's length; x, a, b, base and out 16-byte aligned.
+ *   0 <= num_rows <= 2^24; in_features and out_features positive multiples of 8, at most 2^20;
+ *   rank a multiple of 8 in [8, 128]; 1 <= num_adapters <= 16384; the strides (elements from one
+ *   row to the next) multiples of 8, at least the row's length; x, a, b, base and out 16-byte aligned.
  *   ws: a device workspace of moe_lora_workspace() bytes (256-byte aligned; its content
  *   does not matter). moe_lora_workspace() is 0 where none is needed (few rows; ws may then
  *   be NULL) and where the arguments are invalid (moe_last_error() then says why). */
@@ -599,7 +599,7 @@ moe_status_t moe_lora_add(const moe_lora_t* lora, const void* base, const moe_bf
  *   is outside [0, num_adapters).
  *   token_of_row [num_rows] and expert_offsets [E + 1] int32 as moe_permute writes them;
  *   adapter [T] int32, T = num_tokens (a token_of_row outside [0, T) is no row);
- *   row_adapter [num_rows] int32 out. 1 <= num_experts <= 512, num_rows >= 0,
+ *   row_adapter [num_rows] int32 out. 1 <= num_experts <= 512, 0 <= num_rows < 2^31,
  *   num_adapters * num_experts <= 16384. */
 moe_status_t moe_lora_rows(const int32_t* token_of_row, const int32_t* expert_offsets,
                            const int32_t* adapter, int64_t num_tokens, int64_t num_rows,
@@ -610,7 +610,7 @@ moe_status_t moe_lora_rows(const int32_t* token_of_row, const int32_t* expert_of
  *   h = bf16(silu(gate) * up), silu(g) = g / (1 + exp(-g)), for the rows below
  *   expert_offsets[E] (rows past them untouched).
  *   gate, up [num_rows, I] fp32; h [num_rows, I] bf16 out; I a positive multiple of 8;
- *   expert_offsets [E + 1] int32; 16-byte aligned; num_rows >= 0. */
+ *   expert_offsets [E + 1] int32; 16-byte aligned; 0 <= num_rows < 2^31. */
 moe_status_t moe_swiglu_rows(const float* gate, const float* up, const int32_t* expert_offsets,
                              int num_experts, int64_t num_rows, int intermediate, moe_bf16_t* h,
                              moe_stream_t stream);

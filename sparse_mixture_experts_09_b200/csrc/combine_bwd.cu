@@ -97,8 +97,8 @@ __device__ void zero_dropped(const CombineBwd& c, int32_t* start, int32_t* count
 // The first `owners` blocks look for rows whose slot was taken out, the next token_blocks take a
 // token each (striding), the others zero the pad rows. A token's d_out is read once for its k rows;
 // a thread adds its products in fp32, then the warp and the block add in a fixed order. Bound by
-// HBM: 2 H bytes of d_out and 8 H of every routed row. 4096 tokens, H 4096, 2 slots: 52.5 us, 6.1
-// TB/s (93% of a plain copy's rate); 16 tokens 5.8 us, nearly all of it zeroing the 1120 pad rows.
+// HBM: 2 H bytes of d_out and 8 H of every routed row. 4096 tokens, H 4096, 2 slots: 52 us, 6.1
+// TB/s (94% of a plain copy's rate); 16 tokens 5.6 us, nearly all of it zeroing the 1120 pad rows.
 template <int K>
 __global__ void __launch_bounds__(kThreads) k_combine_bwd(const CombineBwd c, int shift, int token_blocks) {
   pdl_trigger();

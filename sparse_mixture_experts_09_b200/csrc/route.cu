@@ -583,19 +583,23 @@ __device__ __noinline__ void route_in_double(const Routing r, const T* row, cons
 // asked for (both scores rise with the logit, so fp32 is exact); else the values s + bias
 // and the groups' sums are formed in fp32 with the approximate exponential and reciprocal: they
 // give the groups and the candidates, which under sigmoid scores are then ordered by their own
-// s + bias in double. A token with another decision within its error bounds is put aside and
-// routed in double after up to 32 others of the team (a few in ten thousand). Bounds, with
+// s + bias in double. A token with another decision within its error bounds, with more candidates
+// than the team has lanes, or with a group_top above 2 is put aside and routed in double after up to
+// 32 others of the team. Of fp32 logits that is a few tokens in ten thousand, but of bf16 ones, whose
+// values repeat, 2 to 5 in a hundred where 8 slots meet 8 lanes (by logits alone, or with a bias of
+// zeros): 65536 x 64, 8 slots 53 us instead of 25; 6 slots 26. group_top 3: all tokens, 16384 x 256
+// 164 us. Bounds, with
 // u = 2^-24: the exponential is off by 4 u and by 1.5 u |x| for its argument, the reciprocal by
 // 2 u; s (1 - s) is at most 1/4 and |x| s (1 - s) at most 0.23, so a sigmoid is off by less than 5 u
 // (6 u are allowed); |x| e^x is at most 0.37 below 0, so a softmax is off by less than 32 u of the
 // largest probability (its sum of up to 512 terms is a tree of 20 levels); the sum with the bias
 // by u of its value.
 //
-// Bound by instructions, not bytes (some 760 a token at 256 experts with groups and a bias, half
-// the issue slots taken): a team is as narrow as 16 values per lane allow, so that a warp's
+// Bound by instructions and their latency, not bytes (some 760 a token at 256 experts with groups and
+// a bias, 56% of the issue slots at 24% of the warps): a team is as narrow as 16 values per lane allow, so that a warp's
 // instruction serves up to four tokens. Device times: 16384 tokens, 256 experts, 8 slots, sigmoid
-// scores, bias, 4 of 8 groups 24.6 us (17.8 MB: 2.7 us at HBM's rate), without groups 18.7, by
-// logits alone 19.7; 65536 x 64 24 us; one token 3.3 us.
+// scores, bias, 4 of 8 groups 24.3 us (17.8 MB: 2.7 us at HBM's rate), groups by their logits 22.5,
+// without groups 18.9, by logits alone 20.0; 65536 x 64 25 us; one token 3.3 us.
 template <typename T, int L, int V, bool FEW>
 __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
     k_route(const Routing r, const T* __restrict__ logits, const float* __restrict__ bias, int vec,
@@ -748,7 +752,8 @@ __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 4 : V <= 8 ? 3 : 2)
 // adds its experts' p over its tokens in fp32 (every 3552nd at 256 experts, 14208th at 64), the block
 // adds its teams' sums in order in double: E + 1 sums and counts. Bound by latency: few bytes
 // and few steps per token, so the next token's loads go out before this one's sums (65521
-// tokens, 64 experts, 6 slots: 13.2 us with the second pass; 18.4 MB, 2.8 us at HBM's rate).
+// tokens, 64 experts, 6 slots: 13.0 us with the second pass, 14.0 with sigmoid scores; 18.4 MB, 2.8 us at
+// HBM's rate).
 template <typename T, int L, int V, int WARPS>
 __device__ __forceinline__ void block_losses(const Routing& r, const T* __restrict__ logits,
                                              const int32_t* __restrict__ idx,
@@ -914,8 +919,8 @@ __device__ __forceinline__ void finish_cluster(const Routing& r, const double* s
 
 // Little work: one launch, a cluster of 8 blocks of 1024 threads whose first block adds the sums
 // up from their shared memory; no workspace. It saves a launch and an allocation of the caller's
-// (some 4 us), but has 8 SMs only. Device and whole call, one launch / two passes: 4096 x 8
-// 8.2 / 6.7 and 13.0 / 17.1 us, 8192 x 8 11.9 / 7.3 and 13.0 / 17.1, 4096 x 64 10.7 / 7.6 and
+// (some 4 us), but has 8 SMs only: it is the quicker form for single calls, the slower one in a captured
+// graph. Device and whole call with no mask, one launch / two passes: 4096 x 8 8.2 / 6.7 and 13.0 / 17.1 us, 8192 x 8 11.9 / 7.3 and 13.0 / 17.1, 4096 x 64 10.7 / 7.6 and
 // 13.2 / 17.3, 8192 x 64 16.5 / 8.1 and 16.8 / 17.3, 1024 x 256 10.2 / 8.1 and 13.0 / 17.1, 4096 x 256
 // 28.1 / 11.4 and 28.7 / 17.1.
 constexpr int64_t kLossTokens = 8192, kLossLogits = 1 << 18;
@@ -998,8 +1003,10 @@ __global__ void __launch_bounds__(1024) k_losses_end(const Routing r, int blocks
 //   balance: softmax p_e (c_e - sum c p); sigmoid s_e (1 - s_e) (c_e - sum c p) / sum s;
 //   z: 2 d1 / N * logsumexp * softmax_e.
 // A slot's term crosses from its lane to its expert's through shared memory. Bound by
-// instructions (580 a token at 256 experts, 57% of the issue slots): 16384 x 256 with sigmoid scores
-// and losses 17.1 us (34.6 MB: 5.3 us at HBM's rate), 4096 x 8 4.6 us.
+// instructions (600 a token at 256 experts, 57% of the issue slots): 16384 x 256 with sigmoid scores
+// and losses 16.9 us (34.6 MB: 5.3 us at HBM's rate), 4096 x 8 4.4 us. The exponentials are 2^x (see
+// fast_exp2) and the divisions of sums __fdividef (2 units in the last place): some 2 and 1 u more
+// than expf and a rounded division, of the 128 u that a gradient's terms are held to.
 template <typename T, int L, int V>
 __global__ void __launch_bounds__(32 * kWarps, V <= 4 ? 6 : V <= 8 ? 4 : 2)
     k_route_bwd(const Routing r, const T* __restrict__ logits, const int32_t* __restrict__ idx,
